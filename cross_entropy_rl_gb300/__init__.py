@@ -20,6 +20,7 @@ __all__ = [
     "LLError", "load", "lib", "forward", "backward", "forward_backward", "logits_fwd",
     "logits_bwd", "logits_fwd_bwd", "shard_segments", "forward_shard", "lse_merge",
     "backward_shard", "SEGMENT_COLS",
+    "embed_forward", "embed_backward", "policy_loss", "grad_norm", "clip_grads",
     "workspace_size", "check_status", "DTYPE_CODES", "EXPORTS",
 ]
 
@@ -35,6 +36,7 @@ _c_i64 = ctypes.c_int64
 _c_p = ctypes.c_void_p
 _c_int = ctypes.c_int
 _c_size = ctypes.c_size_t
+_c_float = ctypes.c_float
 
 # name -> (restype, argtypes): every symbol the header declares
 EXPORTS = {
@@ -89,6 +91,17 @@ EXPORTS = {
     "ll_profile_enable": (None, [_c_int]),
     "ll_profile_summary": (_c_int, [ctypes.c_char_p, _c_size]),
     "ll_sum_ordered": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_int, _c_p, _c_p]),
+    "ll_embed_forward": (_c_int, [_c_p, _c_i64, _c_int, _c_p, _c_i64, _c_i64, _c_i64, _c_i64,
+                                  _c_float, _c_p, _c_i64, _c_int, _c_p]),
+    "ll_embed_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "ll_embed_backward": (_c_int, [_c_p, _c_i64, _c_int, _c_p, _c_i64, _c_i64, _c_i64, _c_i64,
+                                   _c_float, _c_int, _c_p, _c_i64, _c_int, _c_p, _c_size, _c_p]),
+    "ll_policy_workspace_size": (_c_size, [_c_i64, _c_i64]),
+    "ll_policy_loss": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p,
+                                _c_p, _c_p, _c_size, _c_p]),
+    "ll_grad_norm_workspace_size": (_c_size, [_c_i64]),
+    "ll_grad_norm": (_c_int, [_c_p, _c_i64, _c_p, _c_p, _c_size, _c_p]),
+    "ll_clip_grads": (_c_int, [_c_p, _c_i64, _c_float, _c_int, _c_p, _c_p, _c_size, _c_p]),
 }
 
 
@@ -580,3 +593,241 @@ def backward_shard(grad_logp, hidden, weight, bias, targets, lse, v0, V, *, need
                              _opts(temperature, split_s), _stream(stream))
     _check("ll_backward_shard", st)
     return dh, dW, db
+
+
+# ------------------------------------------------- the rest of a training step
+
+def _rows(t, name, dtypes):
+    """(rows, columns, row stride) of a 2-D tensor whose rows are contiguous."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
+    n, d = t.shape
+    ld = t.stride(0) if n > 1 else d
+    if n and d and ((d > 1 and t.stride(1) != 1) or ld < d):
+        raise ValueError(f"{name}: each row must be contiguous and the rows apart")
+    return n, d, ld
+
+
+def _stream_of(device, stream):
+    """The stream of a call whose tensors lie on `device`, as a handle."""
+    torch = _torch()
+    if stream is None and device.type == "cuda":
+        stream = torch.cuda.current_stream(device)
+    return ctypes.c_void_p(stream.cuda_stream if stream is not None else None)
+
+
+def _used_on(stream, *tensors):
+    """Tensors that torch allocated for a call on a stream of the caller's: the
+    allocator may not hand them out again before that stream is done with them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+
+
+def _float_types():
+    torch = _torch()
+    return torch.float32, torch.float16, torch.bfloat16
+
+
+def embed_forward(weight, tokens, *, scale=1.0, v0=0, out_dtype=None, out=None, stream=None):
+    """out [N, D] = scale * weight[tokens - v0], +0 rows for tokens outside
+    [v0, v0 + V).  weight [V, D] and out may have a row stride.  out_dtype
+    defaults to weight's; FP32 is always possible, and anything from FP32."""
+    torch = _torch()
+    L = load()
+    types = _float_types()
+    V, D, ldw = _rows(weight, "weight", types)
+    dev = weight.device
+    N = tokens.numel() if isinstance(tokens, torch.Tensor) else 0
+    _need(tokens, "tokens", (N,), torch.int64, dev)
+    if out is None:
+        out = torch.empty(N, D, dtype=weight.dtype if out_dtype is None else out_dtype, device=dev)
+        _used_on(stream, out)
+    elif out_dtype is not None and out_dtype != out.dtype:
+        raise TypeError("out_dtype disagrees with the given out")
+    n, d, ldo = _rows(out, "out", types)
+    if (n, d) != (N, D) or out.device != dev:
+        raise ValueError(f"out: {(n, d)} on {out.device}, expected {(N, D)} on {dev}")
+    st = L.ll_embed_forward(_ptr(weight), ldw, _code(weight.dtype), _ptr(tokens), N, D, V, int(v0),
+                            float(scale), _ptr(out), ldo, _code(out.dtype),
+                            _stream_of(dev, stream))
+    _check("ll_embed_forward", st)
+    return out
+
+
+def embed_backward(grad_out, tokens, V, *, scale=1.0, v0=0, dw_dtype=None, accumulate=False,
+                   out=None, workspace=None, stream=None):
+    """grad_weight [V, D] of embed_forward: row v the sum of scale * grad_out[n]
+    over the n with tokens[n] == v0 + v.  dw_dtype (FP32 by default, or
+    grad_out's) is that of `out` when given.  accumulate=True adds into `out`
+    (tied weights: the grad_weight of `backward`)."""
+    torch = _torch()
+    L = load()
+    types = _float_types()
+    N, D, ldg = _rows(grad_out, "grad_out", types)
+    V = int(V)
+    dev = grad_out.device
+    _need(tokens, "tokens", (N,), torch.int64, dev)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs the table to add into (out)")
+        out = torch.empty(V, D, dtype=torch.float32 if dw_dtype is None else dw_dtype, device=dev)
+        _used_on(stream, out)
+    elif dw_dtype is not None and dw_dtype != out.dtype:
+        raise TypeError("dw_dtype disagrees with the given out")
+    v, d, ldw = _rows(out, "out", types)
+    if (v, d) != (V, D) or out.device != dev:
+        raise ValueError(f"out: {(v, d)} on {out.device}, expected {(V, D)} on {dev}")
+    if workspace is None:
+        workspace = _workspace(L.ll_embed_workspace_size(N, D, V), dev)
+        _used_on(stream, workspace)
+    _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+    st = L.ll_embed_backward(_ptr(grad_out), ldg, _code(grad_out.dtype), _ptr(tokens), N, D, V,
+                             int(v0), float(scale), int(bool(accumulate)), _ptr(out), ldw,
+                             _code(out.dtype), _ptr(workspace), workspace.numel(),
+                             _stream_of(dev, stream))
+    _check("ll_embed_backward", st)
+    return out
+
+
+class PolicyOptions(ctypes.Structure):
+    """ll_policy_options of the C ABI."""
+    _fields_ = [("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+                ("kl_coef", ctypes.c_double), ("denominator", ctypes.c_double),
+                ("reserved", ctypes.c_int * 4)]
+
+
+def policy_loss(logp, old_logp, advantages, *, ref_logp=None, mask=None, seq_offsets=None,
+                clip_low=0.2, clip_high=0.2, kl_coef=0.0, denominator=None, out=None,
+                workspace=None, stream=None):
+    """(stats [4], grad_logp [N]), FP32, of the clipped policy loss: stats are
+    the loss, its policy part, the divergence from ref_logp and the clipped
+    share; grad_logp is what `backward` takes.
+
+    mask [N] (bool or uint8): tokens that count.  The loss is the mean over
+    them, or with seq_offsets ([B + 1] int64, on the device) the mean over the
+    sequences of each sequence's mean; denominator replaces the number of
+    tokens (sequences) of this call."""
+    torch = _torch()
+    L = load()
+    N = logp.numel() if isinstance(logp, torch.Tensor) else 0
+    _need(logp, "logp", (N,), torch.float32)
+    dev = logp.device
+    _need(old_logp, "old_logp", (N,), torch.float32, dev)
+    _need(advantages, "advantages", (N,), torch.float32, dev)
+    if ref_logp is not None:
+        _need(ref_logp, "ref_logp", (N,), torch.float32, dev)
+    if mask is not None:
+        _need(mask, "mask", (N,), device=dev, dtypes=(torch.bool, torch.uint8))
+    B = 0
+    if seq_offsets is not None:
+        B = max(seq_offsets.numel() - 1, 0) if isinstance(seq_offsets, torch.Tensor) else 0
+        _need(seq_offsets, "seq_offsets", (B + 1,), torch.int64, dev)
+        if B == 0:
+            raise ValueError("seq_offsets: at least two are needed")
+    if denominator is not None and not float(denominator) > 0:
+        raise ValueError("denominator must be > 0")
+    if out is None:
+        stats = torch.empty(4, dtype=torch.float32, device=dev)
+        grad = torch.empty(N, dtype=torch.float32, device=dev)
+        _used_on(stream, stats, grad)
+    else:
+        stats, grad = out
+    _need(stats, "stats", (4,), torch.float32, dev)
+    _need(grad, "grad_logp", (N,), torch.float32, dev)
+    if workspace is None:
+        workspace = _workspace(L.ll_policy_workspace_size(N, B), dev)
+        _used_on(stream, workspace)
+    _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+    opt = PolicyOptions(float(clip_low), float(clip_high), float(kl_coef),
+                        0.0 if denominator is None else float(denominator))
+    st = L.ll_policy_loss(_ptr(logp), _ptr(old_logp), _ptr(ref_logp), _ptr(advantages),
+                          _ptr(mask), _ptr(seq_offsets), B, N, ctypes.byref(opt), _ptr(stats),
+                          _ptr(grad), _ptr(workspace), workspace.numel(),
+                          _stream_of(dev, stream))
+    _check("ll_policy_loss", st)
+    return stats, grad
+
+
+class Tensor(ctypes.Structure):
+    """ll_tensor of the C ABI."""
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("reserved", ctypes.c_int)]
+
+
+def _tensor_list(tensors):
+    """(ll_tensor array, device) of gradients that each fill their memory
+    without gaps, in any order of their dimensions."""
+    torch = _torch()
+    codes = DTYPE_CODES()
+    arr = (Tensor * len(tensors))()
+    dev = None
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"tensor {i} must be a torch.Tensor")
+        if t.dtype not in codes:
+            raise TypeError(f"tensor {i}: unsupported dtype {t.dtype}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensor {i}: on {t.device}, expected {dev}")
+        if not t.is_contiguous() and not _dense(t):
+            raise ValueError(f"tensor {i}: its elements must fill their memory without gaps")
+        a = arr[i]
+        a.data, a.n, a.dtype = t.data_ptr(), t.numel(), codes[t.dtype]
+    return arr, dev
+
+
+def _dense(t):
+    """Whether some order of the dimensions makes the tensor contiguous."""
+    need = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != need:
+            return False
+        need *= size
+    return True
+
+
+def _norm_call(tensors, norm, workspace, stream):
+    torch = _torch()
+    L = load()
+    arr, dev = _tensor_list(tensors)
+    if dev is None:
+        dev = norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        _used_on(stream, norm)
+    _need(norm, "norm", (), torch.float32, dev)
+    if workspace is None:
+        workspace = _workspace(L.ll_grad_norm_workspace_size(len(arr)), dev)
+        _used_on(stream, workspace)
+    _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+    return L, arr, dev, norm, workspace
+
+
+def grad_norm(tensors, *, out=None, workspace=None, stream=None):
+    """The norm (0-d FP32) of a list of gradients taken as one vector.  Their
+    dtypes may differ; each must fill its memory without gaps."""
+    L, arr, dev, out, workspace = _norm_call(tensors, out, workspace, stream)
+    st = L.ll_grad_norm(arr, len(arr), _ptr(out), _ptr(workspace), workspace.numel(),
+                        _stream_of(dev, stream))
+    _check("ll_grad_norm", st)
+    return out
+
+
+def clip_grads(tensors, max_norm, *, norm=None, workspace=None, stream=None):
+    """Scales a list of gradients in place by min(1, max_norm / (norm + 1e-6))
+    and returns norm: that of the list, or a given one (0-d FP32 on the device:
+    gradients sharded over ranks)."""
+    given = norm is not None
+    L, arr, dev, norm, workspace = _norm_call(tensors, norm, workspace, stream)
+    st = L.ll_clip_grads(arr, len(arr), float(max_norm), int(given), _ptr(norm), _ptr(workspace),
+                         workspace.numel(), _stream_of(dev, stream))
+    _check("ll_clip_grads", st)
+    return norm

@@ -22,7 +22,8 @@ LIB_NAME = "libll_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 
 SOURCES = ["capi.cu", "logits_kernels.cu", "gemm_tc.cu", "gemm_tf32.cu",
-           "aux_kernels.cu", "noalloc.cu"]
+           "aux_kernels.cu", "embed_kernels.cu", "policy_kernels.cu", "grad_kernels.cu",
+           "noalloc.cu"]
 HEADERS = ["ll_device.cuh", "ll_internal.h", "epilogue.cuh", "gemm_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -284,6 +284,39 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
     }
 }
 
+// E consecutive elements of T, moved in vectors of up to 16 bytes when they
+// fill them (the pointer is then aligned to 16 bytes, or to the whole pack if
+// that is smaller), else one by one.
+template <typename T, int E>
+struct Pack {
+    static constexpr int kBytes = E * int(sizeof(T));
+    alignas(kBytes % 16 == 0 ? 16 : kBytes) T e[E];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i)
+                reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
+        } else if constexpr (kBytes == 8) {
+            *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) e[i] = p[i];
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i)
+                reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(e)[i];
+        } else if constexpr (kBytes == 8) {
+            *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) p[i] = e[i];
+        }
+    }
+};
+
 // ------------------------------------------ CTA pairs (cluster of two CTAs)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;

@@ -284,6 +284,62 @@ cudaError_t launch_softmax_part(const float* Z, int64_t ldZ, int64_t rows, int64
                                 void* S, int64_t ldS, int s_dtype, float* tc, float* db_part,
                                 float inv_temp, void* S_lo, uint8_t* lo_flags,
                                 cudaStream_t s);
+// --- embedding lookup and its gradient (embed_kernels.cu) ---------------------
+struct EmbedArgs {
+    const void* rows;       // lookup: the table; gradient: grad_out
+    int64_t ld_rows;
+    int dtype;              // of rows
+    const int64_t* tokens;  // [N]
+    int64_t N, D, V, v0;
+    float scale;
+    void* table;            // lookup: out; gradient: grad_weight
+    int64_t ld_table;
+    int table_dtype;
+};
+cudaError_t launch_embed_fwd(const EmbedArgs& a, cudaStream_t s);
+size_t embed_bwd_bytes(int64_t N, int64_t D, int64_t V);
+cudaError_t launch_embed_sort(const EmbedArgs& a, void* ws, cudaStream_t s);
+cudaError_t launch_embed_bwd(const EmbedArgs& a, int accumulate, void* ws, cudaStream_t s);
+
+// --- policy loss (policy_kernels.cu) -------------------------------------------
+struct PolicyArgs {
+    const float *logp, *old, *ref, *adv;  // ref may be null
+    const uint8_t* mask;                  // or null
+    const int64_t* offs;                  // [n_seqs + 1] or null
+    int64_t n_seqs, N;
+    double log_lo, log_hi;     // log(1 - clip_low), log(1 + clip_high)
+    float bound_lo, bound_hi;  // 1 - clip_low, 1 + clip_high
+    double beta_d, denominator;
+    float beta;
+    float *stats, *grad;
+};
+constexpr int kPolicyBlocks = 1024;  // most blocks, and so partial sums, of the loss kernel
+struct PolicyWs {
+    unsigned long long tokens, full;  // unmasked tokens, sequences that have one
+    unsigned done, pad[3];            // blocks whose partial sums are written
+    double part[3 * kPolicyBlocks];
+};
+size_t policy_ws_bytes(int64_t n_seqs);
+cudaError_t launch_policy_loss(const PolicyArgs& a, void* workspace, cudaStream_t s);
+
+// --- gradient norm and clipping (grad_kernels.cu) ------------------------------
+constexpr int kMaxTensors = 512;           // tensors of one launch
+constexpr int64_t kGradChunk = 16384;      // elements a block takes at a time
+constexpr int kGradBlocksPerSm = 8;
+constexpr int kGradMaxBlocks = 2048;       // most blocks, and so partial sums, of one launch
+struct GradList {
+    const void* data[kMaxTensors];
+    int64_t n[kMaxTensors];
+    int64_t first[kMaxTensors];  // number of the tensor's first chunk
+    uint8_t dtype[kMaxTensors];
+    int64_t chunk, chunks;
+    int count;
+};
+cudaError_t launch_grad_norm(const ll_tensor* t, int64_t count, float* norm, void* ws,
+                             int num_sms, cudaStream_t s);
+cudaError_t launch_grad_clip(const ll_tensor* t, int64_t count, float max_norm, const float* norm,
+                             int num_sms, cudaStream_t s);
+
 cudaError_t launch_unsatisfied_wait(int* flag, int* status, uint64_t wait_ns, cudaStream_t s);
 
 }  // namespace ll

@@ -405,12 +405,153 @@ int ll_sum_ordered(const void* parts, int64_t nparts, int64_t n, int64_t ld, int
                    void* out, void* stream);
 
 /*
+ * The calls around the linear log-probability in a training step: the other
+ * end of the vocabulary matrix (embedding lookup and its gradient), the loss
+ * between ll_forward and ll_backward, and the gradients' norm and clipping.
+ */
+
+/*
+ * Embedding lookup:
+ *   out[n, :] = scale * weight[tokens[n] - v0, :]   if v0 <= tokens[n] < v0 + V
+ *             = +0                                  otherwise
+ * The product is formed in FP32 and rounded once to out_dtype.  v0 = 0 for a
+ * whole table; with a table split over ranks by vocab id, each rank passes its
+ * rows and its v0, and the sum of the ranks' outputs is the whole lookup (one
+ * rank at most gives a row that is not +0).
+ *   weight [V, ldw] dtype, device; row r is vocab id v0 + r; columns [D, ldw)
+ *          are ignored.  ldw >= D.
+ *   tokens [N] int64, device.
+ *   out    [N, ld_out] of out_dtype, device (columns [0, D) written, the rest
+ *          untouched; ld_out >= D).  out_dtype is dtype, LL_F32, or anything
+ *          when dtype is LL_F32.  out may not overlap weight.
+ * Pointers need the alignment of their elements only; rows that start on
+ * 16-byte boundaries are read and written 16 bytes at a time.
+ * scale must be finite.  N == 0 launches nothing.  D >= 1, V >= 1.
+ */
+int ll_embed_forward(const void* weight, int64_t ldw, int dtype, const int64_t* tokens,
+                     int64_t N, int64_t D, int64_t V, int64_t v0, float scale, void* out,
+                     int64_t ld_out, int out_dtype, void* stream);
+
+/* Workspace bytes of ll_embed_backward (256-byte aligned); 0 when N == 0. */
+size_t ll_embed_workspace_size(int64_t N, int64_t D, int64_t V);
+
+/*
+ * Gradient of the embedding lookup:
+ *   G[v, :] = scale * sum of grad_out[n, :] over the n with tokens[n] == v0 + v
+ *   accumulate = 0: grad_weight = G (rows of no token are +0)
+ *   accumulate = 1: grad_weight += G (rows of no token are not touched): tied
+ *     weights add into the grad_weight that ll_backward wrote, and
+ *     micro-batches add into one table
+ *   grad_out    [N, ldg] dtype, device; ldg >= D.
+ *   grad_weight [V, ldw] of dw_dtype (dtype or LL_F32), device (columns
+ *               [0, D) written); ldw >= D; it may not overlap grad_out.
+ * The rows of one token are added in ascending n, in FP32, in pieces of a
+ * fixed number of rows (a function of N alone) whose sums are then added in a
+ * fixed order; one rounding to dw_dtype.  A row of grad_weight depends on the
+ * rows of its own token alone, and runs give the same bits.
+ * N == 0 with accumulate = 0 fills grad_weight with +0.
+ */
+int ll_embed_backward(const void* grad_out, int64_t ldg, int dtype, const int64_t* tokens,
+                      int64_t N, int64_t D, int64_t V, int64_t v0, float scale, int accumulate,
+                      void* grad_weight, int64_t ldw, int dw_dtype, void* workspace,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * Options of ll_policy_loss.  NULL means clip_low = clip_high = 0.2 and zeros.
+ *   clip_low     in [0, 1): lower bound 1 - clip_low of the ratio.
+ *   clip_high    >= 0 and finite: upper bound 1 + clip_high.
+ *   kl_coef      >= 0 and finite: weight of the divergence from the reference
+ *                policy; it needs ref_logp when it is not 0.
+ *   denominator  > 0: the divisor of the sums, for a loss that is a mean over
+ *                more than this call (micro-batches, ranks); 0: counted here.
+ *   reserved     must be 0.
+ */
+typedef struct {
+    double clip_low, clip_high, kl_coef, denominator;
+    int reserved[4];
+} ll_policy_options;
+
+/* Workspace bytes of ll_policy_loss (256-byte aligned); 0 when N == 0. */
+size_t ll_policy_workspace_size(int64_t N, int64_t n_seqs);
+
+/*
+ * Clipped policy loss over sampled tokens, with its gradient: logp from
+ * ll_forward in, grad_logp for ll_backward out.  Per token, with
+ * delta = logp - old_logp, r = exp(delta), d = ref_logp - logp:
+ *   clipped = (A > 0 and delta > log(1 + clip_high)) or
+ *             (A < 0 and delta < log(1 - clip_low))
+ *   p = -A * (clipped ? the bound : r)     (-min(r A, clamp(r) A); 0 if A == 0)
+ *   k = exp(d) - d - 1                     (0 without ref_logp)
+ *   loss = sum_t w_t (p_t + kl_coef k_t)
+ *   grad_logp_t = w_t ((clipped ? 0 : -A r) - kl_coef (exp(d) - 1))
+ * Weights: w_t = 0 where mask_t == 0, else
+ *   seq_offsets == NULL: 1 / denominator (default: the number of unmasked tokens)
+ *   else 1 / (unmasked tokens of t's sequence * denominator) (default: the
+ *   number of sequences that have an unmasked token).
+ * What a masked token holds (an infinity, a NaN) is not used: its grad_logp
+ * is +0.  If no token is unmasked, all outputs are +0.
+ *   logp, old_logp, advantages [N] float, device; ref_logp [N] or NULL.
+ *   mask [N] bytes (0 = left out), device, or NULL (no token is left out).
+ *   seq_offsets [n_seqs + 1] int64, device, ascending, or NULL (n_seqs == 0):
+ *     sequence b is the tokens [seq_offsets[b], seq_offsets[b + 1]); it may be
+ *     empty.  Tokens in no sequence are left out.
+ *   stats [4] float, device (written): loss, sum w p, sum w k, sum of w over
+ *     the clipped tokens.
+ *   grad_logp [N] float, device (written).
+ * The clipping border is decided on delta in 64 bits; sums over tokens are
+ * held in 64 bits and added in a fixed order.  N == 0 writes stats = 0.
+ */
+int ll_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,
+                   const float* advantages, const uint8_t* mask, const int64_t* seq_offsets,
+                   int64_t n_seqs, int64_t N, const ll_policy_options* opt, float* stats,
+                   float* grad_logp, void* workspace, size_t ws_bytes, void* stream);
+
+/* One tensor of a list: n elements of dtype at data (device), in any order.
+ * data may be NULL when n == 0.  reserved must be 0.  The list itself is host
+ * memory and is read during the call only. */
+typedef struct {
+    void* data;
+    int64_t n;
+    int dtype;
+    int reserved;
+} ll_tensor;
+
+/* Workspace bytes of ll_grad_norm and ll_clip_grads for `count` tensors
+ * (256-byte aligned). */
+size_t ll_grad_norm_workspace_size(int64_t count);
+
+/*
+ * Norm of all gradients as one vector: norm[0] = sqrt(sum of squares over
+ * every element of every tensor), FP32 on the device.  The squares are summed
+ * in FP32 over short runs and in 64 bits beyond; runs whose largest element
+ * is outside [2^-50, 2^55] in magnitude are squared in 64 bits, so nothing
+ * overflows or vanishes on the way.  A NaN or an infinity gives NaN or
+ * infinity.  The same list gives the same bits.  No tensors: norm = 0.
+ */
+int ll_grad_norm(const ll_tensor* tensors, int64_t count, float* norm, void* workspace,
+                 size_t ws_bytes, void* stream);
+
+/*
+ * Clipping in place: every element times coef = min(1, max_norm / (norm +
+ * 1e-6)), in FP32 and rounded once to its tensor's dtype; with coef == 1
+ * nothing is written.  A norm of infinity gives coef = 0, a NaN gives NaN.
+ *   norm_given = 0: norm[0] is computed as in ll_grad_norm and written.
+ *   norm_given = 1: norm[0] (device) is read: for a norm over more than this
+ *     list (gradients sharded over ranks).  No workspace.
+ * max_norm > 0 (infinity: no clipping).  No two tensors may overlap
+ * (LL_ERR_INVALID_ARG).
+ */
+int ll_clip_grads(const ll_tensor* tensors, int64_t count, float max_norm, int norm_given,
+                  float* norm, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Tracing.  ll_launch_count(): number of kernels this library has launched
  * in the process.  ll_profile_enable(1) clears earlier records and brackets
  * every phase of later calls (fwd_gemm, lse_merge, token_sort,
  * recompute_gemm, softmax_part, lo_plan, transpose_h, grad_gemm
  * (grad_hidden and grad_weight tiles), db_sums, logits_fwd, logits_bwd,
- * logits_fused, sum_ordered; an _f32 suffix
+ * logits_fused, sum_ordered, embed_fwd, embed_sort, embed_grad, policy_loss,
+ * grad_norm, grad_clip; an _f32 suffix
  * marks the GEMMs of FP32 operands, 3 x TF32 on the tensor cores) with CUDA
  * events on the call's
  * stream; ll_profile_enable(0) stops recording.  ll_profile_summary()
