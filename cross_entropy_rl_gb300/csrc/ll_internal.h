@@ -317,11 +317,13 @@ struct PolicyArgs {
     float beta;
     float *stats, *grad;
 };
-constexpr int kPolicyBlocks = 1024;  // most blocks, and so partial sums, of the loss kernel
+constexpr int kPolicyBlocks = 304;  // most blocks, and so partial sums, of the loss kernel
 struct PolicyWs {
-    unsigned long long tokens, full;  // unmasked tokens, sequences that have one
-    unsigned done, pad[3];            // blocks whose partial sums are written
-    double part[3 * kPolicyBlocks];
+    float2 part[3 * kPolicyBlocks];  // hi, lo
+    int tokens[kPolicyBlocks];  // unmasked tokens of each block
+    unsigned done, pad[3];      // blocks whose partial sums are written
+    unsigned long long full;    // sequences that have an unmasked token
+    unsigned long long pad2;    // the sequences' counts follow
 };
 size_t policy_ws_bytes(int64_t n_seqs);
 cudaError_t launch_policy_loss(const PolicyArgs& a, void* workspace, cudaStream_t s);

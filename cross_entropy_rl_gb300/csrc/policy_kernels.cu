@@ -16,22 +16,72 @@
 namespace ll {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kSlots = 8;                 // tokens of a lane of one plain FP32 sum
+constexpr int kSmallCtas = 8;             // CTAs of the one-launch path's cluster
+constexpr int kSmallThreads = 512;
+constexpr int64_t kSmallTokens = 4096;    // most tokens (and sequences) of the one-launch path
 
-// Sequence of token t: the last b with offs[b] <= t, -1 if t lies in none.
-// Whatever the offsets hold, the result is in [-1, n_seqs).
-__device__ __forceinline__ int64_t seq_of(const int64_t* __restrict__ offs, int64_t n_seqs,
-                                          int64_t t) {
-    int64_t lo = 0, hi = n_seqs + 1;  // first index with offs > t
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (offs[mid] <= t)
-            lo = mid + 1;
-        else
-            hi = mid;
+// Sequences of 32 tokens at a time, for a warp that walks along the tokens.
+// Its lanes hold the ends of the next 32 sequences; where they are not known
+// (the start, or past them) the warp searches, 32 probes a step.  The sequence
+// of token t is the last b with offs[b] <= t, or -1 if t lies in none; whatever
+// the offsets hold, it is in [-1, n_seqs).
+struct SeqWalk {
+    int base = -2;         // lane l holds the end of sequence base + l; -2: nothing
+    int ends = 0;
+    bool uniform = false;  // the 32 tokens lie in one sequence
+
+    __device__ __forceinline__ static int offset(const PolicyArgs& a, int64_t i) {
+        const int64_t o = a.offs[i];
+        return o < 0 ? 0 : o > 0x7fffffff ? 0x7fffffff : static_cast<int>(o);
     }
-    return lo - 1 < n_seqs ? lo - 1 : -1;
-}
+    // How many of the n_seqs + 1 offsets are <= t.
+    __device__ static int64_t search(const PolicyArgs& a, int t, int lane) {
+        int64_t lo = 0, hi = a.n_seqs + 1;
+        while (lo < hi) {
+            const int64_t step = (hi - lo + 31) / 32, p = lo + lane * step;
+            const int c = __popc(__ballot_sync(0xffffffffu, p < hi && offset(a, p) <= t));
+            if (c == 0) break;
+            const int64_t at = lo + (c - 1) * step;
+            lo = at + 1;
+            hi = at + step < hi ? at + step : hi;
+        }
+        return lo;
+    }
+    __device__ __forceinline__ int at(const PolicyArgs& a, int64_t t64, int lane) {
+        const int t0 = static_cast<int>(t64), t1 = t0 + 31, t = t0 + lane;
+        if (base == -2 || __shfl_sync(0xffffffffu, ends, 31) <= t1) {
+            base = static_cast<int>(search(a, t0, lane)) - 1;
+            const int64_t i = int64_t(base) + 1 + lane;
+            ends = i <= a.n_seqs ? offset(a, i) : 0x7fffffff;
+        }
+        const unsigned m0 = __ballot_sync(0xffffffffu, ends <= t0);
+        const unsigned m1 = __ballot_sync(0xffffffffu, ends <= t1);
+        uniform = m0 == m1;
+        int64_t b;
+        if (uniform) {
+            b = int64_t(base) + __popc(m0);
+        } else if (m1 != ~0u) {
+            int n = 0;  // ends <= t
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1)
+                if (__shfl_sync(0xffffffffu, ends, n + s - 1) <= t) n += s;
+            b = int64_t(base) + n;
+        } else {  // 32 ends or more among 32 tokens
+            int64_t lo = 0, hi = a.n_seqs + 1;
+            while (lo < hi) {
+                const int64_t mid = (lo + hi) >> 1;
+                if (offset(a, mid) <= t)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            b = lo - 1;
+        }
+        return b < a.n_seqs ? static_cast<int>(b) : -1;
+    }
+};
 
 // exp(d) - d - 1.  For small |d| the exponential's rounding alone (6e-8) would
 // be more than the result (d^2 / 2), so there it is d^2 times the Taylor
@@ -89,91 +139,329 @@ __device__ __forceinline__ Token token_loss(const PolicyArgs& a, float logp, flo
     return t;
 }
 
-__device__ __forceinline__ double warp_sum(double x) {
+// Groups of 32 tokens of warp `me` of `warps`: a run, so that a warp walks
+// along the sequences.
+struct Groups {
+    int64_t beg, end;
+    __device__ Groups(int64_t N, int64_t me, int64_t warps) {
+        const int64_t all = (N + 31) / 32, per = (all + warps - 1) / warps;
+        beg = me * per < all ? me * per : all;
+        end = beg + per < all ? beg + per : all;
+    }
+};
+
+__device__ __forceinline__ bool unmasked(const PolicyArgs& a, int64_t t) {
+    return t < a.N && (!a.mask || a.mask[t]);
+}
+
+// Unmasked tokens of a warp's groups (no sequences).
+__device__ __forceinline__ int count_tokens(const PolicyArgs& a, const Groups& g) {
+    int n = 0;
+#pragma unroll 4
+    for (int64_t i = g.beg; i < g.end; ++i) n += unmasked(a, i * 32 + (threadIdx.x & 31));
+    return __reduce_add_sync(0xffffffffu, n);
+}
+
+// Unmasked tokens per sequence, and sequences that have one.  Integer atomics:
+// the same counts in any order.
+__device__ __forceinline__ void count_sequences(const PolicyArgs& a, const Groups& g,
+                                                PolicyWs* __restrict__ ws,
+                                                int* __restrict__ seq_count) {
+    const int lane = threadIdx.x & 31;
+    SeqWalk walk;
+    int held = -1, count = 0;  // not yet added
+    auto flush = [&]() {
+        if (count && lane == 0 && atomicAdd(seq_count + held, count) == 0)
+            atomicAdd(&ws->full, 1ull);
+        count = 0;
+    };
+#pragma unroll 1
+    for (int64_t i = g.beg; i < g.end; ++i) {
+        const bool in = unmasked(a, i * 32 + lane);
+        const int b = walk.at(a, i * 32, lane);
+        if (walk.uniform) {
+            const unsigned m = __ballot_sync(0xffffffffu, in && b >= 0);
+            if (b != held) flush();
+            held = b;
+            count += __popc(m);
+        } else {
+            // one lane adds for all of its sequence
+            const int s = in ? b : -1;
+            const unsigned peers = __match_any_sync(0xffffffffu, s);
+            if (s >= 0 && lane == __ffs(peers) - 1 && atomicAdd(seq_count + s, __popc(peers)) == 0)
+                atomicAdd(&ws->full, 1ull);
+        }
+    }
+    flush();
+}
+
+// A sum held as hi + lo, |lo| at most half a step of hi: about 48 bits from
+// FP32 additions.  In FP64, of which an SM starts two operations a cycle, the
+// sums and weights kept that unit 77% busy and made most of the kernel's time
+// (48 us cold for a million tokens).  The _rn forms keep the compiler from fusing.
+struct Pair {
+    float hi, lo;
+};
+
+__device__ __forceinline__ float finite_or_0(float e, float of) {
+    return fabsf(of) < INFINITY ? e : 0.f;
+}
+
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    const float s = __fadd_rn(a.hi, b.hi);
+    const float t = __fsub_rn(s, a.hi);
+    float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+    e = finite_or_0(__fadd_rn(e, __fadd_rn(a.lo, b.lo)), s);
+    const float hi = __fadd_rn(s, e);
+    return {hi, finite_or_0(__fsub_rn(e, __fsub_rn(hi, s)), hi)};
+}
+
+// x times the weight w.
+__device__ __forceinline__ Pair times(float x, Pair w) {
+    const float p = __fmul_rn(x, w.hi);
+    return {p, finite_or_0(fmaf(x, w.lo, fmaf(x, w.hi, -p)), p)};
+}
+
+__device__ __forceinline__ Pair pair_of(double x) {
+    const float hi = static_cast<float>(x);
+    return {hi, static_cast<float>(x - hi)};
+}
+
+// one / c: an FP32 quotient and its remainder's.
+__device__ __forceinline__ Pair per_token(Pair one, int c) {
+    const float n = static_cast<float>(c), rest = static_cast<float>(c - static_cast<int>(n));
+    const float q = __fdiv_rn(one.hi, n);
+    return {q, __fdiv_rn(fmaf(-q, n, one.hi) + one.lo - q * rest, n)};
+}
+
+__device__ __forceinline__ Pair warp_sum(Pair x) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = 16; o > 0; o >>= 1)
+        x = add(x, Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
     return x;
 }
 
-// Counts: unmasked tokens (in a sequence), per sequence, and sequences that
-// have one.  Integer atomics: the same counts in any order.
+// Gradients of a warp's groups; adds to s[0..2] the lane's share of the sums.
+// FP32 sums, unweighted, are over kSlots tokens of one sequence at most.  The
+// next group's tokens are loaded ahead, the first ahead of `counted`, which
+// gives 1 / denominator once the counts are there; the loop is kept small,
+// since in a short call its instructions are fetched cold.
+template <typename F>
+__device__ __forceinline__ void loss_tokens(const PolicyArgs& a, const F& counted,
+                                            const int* __restrict__ seq_count, const Groups& g,
+                                            Pair (&s)[3]) {
+    const int lane = threadIdx.x & 31;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    bool in = false;
+    auto fetch = [&](int64_t i) {
+        const int64_t t = i * 32 + lane;
+        in = i < g.end && unmasked(a, t);
+        if (!in) return;
+        x[0] = a.logp[t];
+        x[1] = a.old[t];
+        if (a.ref) x[2] = a.ref[t];
+        x[3] = a.adv[t];
+    };
+    fetch(g.beg);
+    const Pair one = counted();
+    SeqWalk walk;
+    int held = -1, slots = 0;
+    Pair w = a.offs ? Pair{0.f, 0.f} : one;
+    float f[3] = {0.f, 0.f, 0.f};
+    auto flush = [&]() {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            s[j] = add(s[j], times(f[j], w));
+            f[j] = 0.f;
+        }
+        slots = 0;
+    };
+#pragma unroll 1
+    for (int64_t i = g.beg; i < g.end; ++i) {
+        const float logp = x[0], old = x[1], ref = x[2], adv = x[3];
+        bool use = in;
+        fetch(i + 1);
+        const int64_t t = i * 32 + lane;
+        if (a.offs) {
+            const int b = walk.at(a, i * 32, lane);
+            if (b != held) {
+                if (held >= 0) flush();
+                held = b;
+                const int c = b >= 0 ? __ldcg(seq_count + b) : 0;
+                w = c > 0 ? per_token(one, c) : Pair{0.f, 0.f};
+            }
+            if (b < 0) use = false;
+        }
+        float grad = 0.f;
+        if (use) {
+            const Token k = token_loss(a, logp, old, ref, adv);
+            grad = w.hi * k.grad + 0.f;
+            f[0] += k.p;
+            f[1] += k.k;
+            f[2] += k.clipped ? 1.f : 0.f;
+        }
+        if (t < a.N) a.grad[t] = grad;
+        if (++slots == kSlots) flush();
+    }
+    flush();
+}
+
+// Sums of the block's s[0..2] in out[0..2], by a fixed tree.
+template <int kBlock>
+__device__ void block_sums(Pair (&s)[3], Pair* out) {
+    __shared__ Pair all[3][kBlock / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        s[j] = warp_sum(s[j]);
+        if (lane == 0) all[j][warp] = s[j];
+    }
+    __syncthreads();
+    if (warp < 3) {
+        const Pair x = warp_sum(lane < kBlock / 32 ? all[warp][lane] : Pair{0.f, 0.f});
+        if (lane == 0) out[warp] = x;
+    }
+}
+
+// 1 / denominator, of `counted` tokens or sequences where it is not given.
+__device__ __forceinline__ Pair weight(const PolicyArgs& a, unsigned long long counted) {
+    const double n = a.denominator > 0 ? a.denominator : static_cast<double>(counted);
+    return n > 0 ? pair_of(1.0 / n) : Pair{0.f, 0.f};
+}
+
+__device__ __forceinline__ Pair load_pair(const PolicyWs* ws, int i) {
+    const float2 x = __ldcg(&ws->part[i]);
+    return {x.x, x.y};
+}
+
+__device__ __forceinline__ void write_stats(const PolicyArgs& a, const Pair* s) {
+    const double p = double(s[0].hi) + s[0].lo, k = double(s[1].hi) + s[1].lo;
+    a.stats[0] = static_cast<float>(p + a.beta_d * k);
+    a.stats[1] = s[0].hi;
+    a.stats[2] = s[1].hi;
+    a.stats[3] = s[2].hi;
+}
+
+__device__ __forceinline__ Groups grid_groups(const PolicyArgs& a) {
+    return Groups(a.N, blockIdx.x * int64_t(kThreads / 32) + (threadIdx.x >> 5),
+                  int64_t(gridDim.x) * (kThreads / 32));
+}
+
 __global__ void __launch_bounds__(kThreads) policy_count_kernel(const __grid_constant__ PolicyArgs a,
                                                                 PolicyWs* __restrict__ ws,
                                                                 int* __restrict__ seq_count) {
-    const int64_t stride = int64_t(gridDim.x) * kThreads;
-    unsigned long long mine = 0;
-    for (int64_t t = blockIdx.x * int64_t(kThreads) + threadIdx.x; t < a.N; t += stride) {
-        if (a.mask && !a.mask[t]) continue;
-        if (a.offs) {
-            const int64_t b = seq_of(a.offs, a.n_seqs, t);
-            if (b < 0) continue;
-            if (atomicAdd(seq_count + b, 1) == 0) atomicAdd(&ws->full, 1ull);
-        }
-        ++mine;
+    const Groups g = grid_groups(a);
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (blockIdx.x == 0 && threadIdx.x == 0) ws->done = 0;
+    if (a.offs) {
+        count_sequences(a, g, ws, seq_count);
+    } else {
+        __shared__ int all;
+        if (threadIdx.x == 0) all = 0;
+        __syncthreads();
+        const int n = count_tokens(a, g);
+        if (n && (threadIdx.x & 31) == 0) atomicAdd(&all, n);
+        __syncthreads();
+        if (threadIdx.x == 0) ws->tokens[blockIdx.x] = all;
     }
-    if (mine) atomicAdd(&ws->tokens, mine);
 }
 
-__global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_constant__ PolicyArgs a,
-                                                               PolicyWs* __restrict__ ws,
-                                                               const int* __restrict__ seq_count) {
-    __shared__ double part[3][kThreads / 32];
+__global__ void __launch_bounds__(kThreads, 2) policy_loss_kernel(const __grid_constant__ PolicyArgs a,
+                                                                  PolicyWs* __restrict__ ws,
+                                                                  const int* __restrict__ seq_count) {
     __shared__ bool last;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const double n = a.denominator > 0 ? a.denominator
-                                       : static_cast<double>(a.offs ? ws->full : ws->tokens);
-    const int64_t stride = int64_t(gridDim.x) * kThreads;
-    double sp = 0, sk = 0, sc = 0;
-    for (int64_t t = blockIdx.x * int64_t(kThreads) + threadIdx.x; t < a.N; t += stride) {
-        int64_t b = 0;
-        bool in = !a.mask || a.mask[t];
-        if (in && a.offs) {
-            b = seq_of(a.offs, a.n_seqs, t);
-            in = b >= 0;
-        }
-        if (!in) {
-            a.grad[t] = 0.f;
-            continue;
-        }
-        const double dw = 1.0 / (a.offs ? n * seq_count[b] : n);
-        const float w = static_cast<float>(dw);
-        const Token k = token_loss(a, a.logp[t], a.old[t], a.ref ? a.ref[t] : 0.f, a.adv[t]);
-        a.grad[t] = w * k.grad + 0.f;
-        sp += dw * k.p;
-        sk += dw * k.k;
-        sc += k.clipped ? dw : 0.0;
-    }
-    sp = warp_sum(sp);
-    sk = warp_sum(sk);
-    sc = warp_sum(sc);
-    if (lane == 0) {
-        part[0][warp] = sp;
-        part[1][warp] = sk;
-        part[2][warp] = sc;
-    }
-    __syncthreads();
-    if (threadIdx.x < 3) {
-        double s = 0;
-        for (int i = 0; i < kThreads / 32; ++i) s += part[threadIdx.x][i];
-        ws->part[3 * blockIdx.x + threadIdx.x] = s;
-        __threadfence();
-    }
+    __shared__ Pair one;
+    Pair s[3] = {};
+    loss_tokens(
+        a,
+        [&]() {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (threadIdx.x < 32) {
+                unsigned long long n = 0;
+                if (a.offs) {
+                    n = ws->full;
+                } else {
+                    int c = 0;  // of up to ten blocks, each of fewer than 2^31 / gridDim.x tokens
+                    for (unsigned i = threadIdx.x; i < gridDim.x; i += 32) c += ws->tokens[i];
+                    n = __reduce_add_sync(0xffffffffu, c);
+                }
+                if (threadIdx.x == 0) one = weight(a, n);
+            }
+            __syncthreads();
+            return one;
+        },
+        seq_count, grid_groups(a), s);
+    block_sums<kThreads>(s, reinterpret_cast<Pair*>(ws->part) + 3 * blockIdx.x);
+    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) last = atomicAdd(&ws->done, 1u) == gridDim.x - 1;
     __syncthreads();
-    if (!last || threadIdx.x >= 32) return;
+    if (!last) return;
     __threadfence();
-    double s[3] = {0, 0, 0};
-    for (unsigned i = lane; i < gridDim.x; i += 32)
 #pragma unroll
-        for (int j = 0; j < 3; ++j) s[j] += __ldcg(&ws->part[3 * i + j]);
+    for (int j = 0; j < 3; ++j)
+        s[j] = threadIdx.x < gridDim.x ? load_pair(ws, 3 * threadIdx.x + j) : Pair{0.f, 0.f};
+    static_assert(kPolicyBlocks <= kThreads, "a thread per partial sum");
+    __shared__ Pair sums[3];
+    block_sums<kThreads>(s, sums);
+    __syncthreads();
+    if (threadIdx.x == 0) write_stats(a, sums);
+}
+
+// Both passes, and the clearing of the counts, in one cluster: few tokens are
+// bound by the launches, not by what eight SMs can do.
+__global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kSmallThreads)
+    policy_small_kernel(const __grid_constant__ PolicyArgs a, PolicyWs* __restrict__ ws,
+                        int* __restrict__ seq_count) {
+    __shared__ Pair one;
+    __shared__ int warp_tokens[kSmallThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Groups g(a.N, blockIdx.x * (kSmallThreads / 32) + warp, kSmallCtas * (kSmallThreads / 32));
+    if (a.offs) {
+        for (int64_t i = blockIdx.x * kSmallThreads + threadIdx.x; i < a.n_seqs;
+             i += kSmallCtas * kSmallThreads)
+            seq_count[i] = 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0) ws->full = 0;
+        __syncthreads();
+        cluster_barrier();
+        count_sequences(a, g, ws, seq_count);
+        __syncthreads();
+        cluster_barrier();
+        if (threadIdx.x == 0) one = weight(a, __ldcg(&ws->full));
+    } else {
+        const int n = count_tokens(a, g);
+        if (lane == 0) warp_tokens[warp] = n;
+        __syncthreads();
+        cluster_barrier();
+        if (warp == 0) {
+            int all = 0;
 #pragma unroll
-    for (int j = 0; j < 3; ++j) s[j] = warp_sum(s[j]);
-    if (lane == 0) {
-        a.stats[0] = static_cast<float>(s[0] + a.beta_d * s[1]);
-        a.stats[1] = static_cast<float>(s[0]);
-        a.stats[2] = static_cast<float>(s[1]);
-        a.stats[3] = static_cast<float>(s[2]);
+            for (int i = 0; i < kSmallCtas * (kSmallThreads / 32) / 32; ++i) {
+                const int w = i * 32 + lane;
+                int c;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                             : "=r"(c)
+                             : "r"(cluster_addr(warp_tokens + w % (kSmallThreads / 32),
+                                                w / (kSmallThreads / 32))));
+                all += c;
+            }
+            all = __reduce_add_sync(0xffffffffu, all);
+            if (lane == 0) one = weight(a, all);
+        }
+    }
+    __syncthreads();
+    Pair s[3] = {};
+    loss_tokens(a, [&]() { return one; }, seq_count, g, s);
+    block_sums<kSmallThreads>(s, reinterpret_cast<Pair*>(ws->part) + 3 * blockIdx.x);
+    __syncthreads();
+    cluster_barrier();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        for (int j = 0; j < 3; ++j) {
+            s[j] = load_pair(ws, j);
+            for (int i = 1; i < kSmallCtas; ++i) s[j] = add(s[j], load_pair(ws, 3 * i + j));
+        }
+        write_stats(a, s);
     }
 }
 
@@ -184,14 +472,29 @@ size_t policy_ws_bytes(int64_t n_seqs) { return sizeof(PolicyWs) + size_t(n_seqs
 cudaError_t launch_policy_loss(const PolicyArgs& a, void* workspace, cudaStream_t s) {
     PolicyWs* ws = static_cast<PolicyWs*>(workspace);
     int* seq_count = reinterpret_cast<int*>(ws + 1);
+    if (a.N <= kSmallTokens && a.n_seqs <= kSmallTokens) {
+        note_launches(1);
+        policy_small_kernel<<<kSmallCtas, kSmallThreads, 0, s>>>(a, ws, seq_count);
+        return cudaGetLastError();
+    }
     note_launches(2);
-    cudaError_t e = cudaMemsetAsync(ws, 0, policy_ws_bytes(a.n_seqs), s);
-    if (e != cudaSuccess) return e;
+    if (a.offs) {
+        const cudaError_t e = cudaMemsetAsync(&ws->full, 0, 16 + size_t(a.n_seqs) * 4, s);
+        if (e != cudaSuccess) return e;
+    }
     const int64_t blocks = (a.N + kThreads - 1) / kThreads;
     const unsigned grid = static_cast<unsigned>(blocks < kPolicyBlocks ? blocks : kPolicyBlocks);
     policy_count_kernel<<<grid, kThreads, 0, s>>>(a, ws, seq_count);
-    policy_loss_kernel<<<grid, kThreads, 0, s>>>(a, ws, seq_count);
-    return cudaGetLastError();
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, policy_loss_kernel, a, ws, static_cast<const int*>(seq_count));
 }
 
 }  // namespace ll
