@@ -13,6 +13,7 @@ raises when the library is missing or a call returns an error status.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -596,43 +597,72 @@ def backward_shard(grad_logp, hidden, weight, bias, targets, lse, v0, V, *, need
 
 
 # ------------------------------------------------- the rest of a training step
+# Calls of a few microseconds: pointers go to ctypes as plain integers, and the
+# checks build nothing unless they fail.
 
-def _rows(t, name, dtypes):
+def _rows(t, name):
     """(rows, columns, row stride) of a 2-D tensor whose rows are contiguous."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
+    if t.dtype not in _codes():
+        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {tuple(_codes())}")
     n, d = t.shape
-    ld = t.stride(0) if n > 1 else d
-    if n and d and ((d > 1 and t.stride(1) != 1) or ld < d):
+    if t.is_contiguous():
+        return n, d, d
+    ld, one = t.stride()
+    if n <= 1:
+        ld = d
+    if (d > 1 and one != 1) or ld < d:
         raise ValueError(f"{name}: each row must be contiguous and the rows apart")
     return n, d, ld
 
 
+def _vector(t, name, n, dtype, device):
+    """Raise unless t is a contiguous [n] tensor of `dtype` on `device`."""
+    torch = _torch()
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 1 and
+            t.shape[0] == n and t.device == device and t.is_contiguous()):
+        _need(t, name, (n,), dtype, device)
+
+
+_CODES: dict = {}
+
+
+def _codes():
+    """torch dtype -> ll_dtype code."""
+    if not _CODES:
+        _CODES.update(DTYPE_CODES())
+    return _CODES
+
+
 def _stream_of(device, stream):
     """The stream of a call whose tensors lie on `device`, as a handle."""
-    torch = _torch()
-    if stream is None and device.type == "cuda":
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream if stream is not None else None)
-
-
-def _used_on(stream, *tensors):
-    """Tensors that torch allocated for a call on a stream of the caller's: the
-    allocator may not hand them out again before that stream is done with them."""
     if stream is not None:
-        for t in tensors:
-            if t is not None and t.is_cuda:
-                t.record_stream(stream)
+        return stream.cuda_stream
+    if device.type != "cuda":
+        return None  # the call itself then fails: no device memory
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
-def _float_types():
+def _new(shape, dtype, device, stream):
+    """A new tensor for a call.  On a stream of the caller's the allocator may
+    not hand it out again before that stream is done with it."""
+    t = _torch().empty(shape, dtype=dtype, device=device)
+    if stream is not None and t.is_cuda:
+        t.record_stream(stream)
+    return t
+
+
+def _scratch(workspace, nbytes, device, stream):
+    """The given workspace, checked, or a new one."""
     torch = _torch()
-    return torch.float32, torch.float16, torch.bfloat16
+    if workspace is None:
+        return _new((max(nbytes, 256),), torch.uint8, device, stream)
+    _vector(workspace, "workspace", workspace.numel(), torch.uint8, device)
+    return workspace
 
 
 def embed_forward(weight, tokens, *, scale=1.0, v0=0, out_dtype=None, out=None, stream=None):
@@ -641,23 +671,28 @@ def embed_forward(weight, tokens, *, scale=1.0, v0=0, out_dtype=None, out=None, 
     defaults to weight's; FP32 is always possible, and anything from FP32."""
     torch = _torch()
     L = load()
-    types = _float_types()
-    V, D, ldw = _rows(weight, "weight", types)
+    codes = _codes()
+    V, D, ldw = _rows(weight, "weight")
     dev = weight.device
-    N = tokens.numel() if isinstance(tokens, torch.Tensor) else 0
-    _need(tokens, "tokens", (N,), torch.int64, dev)
+    N = tokens.shape[0] if isinstance(tokens, torch.Tensor) and tokens.dim() else 0
+    _vector(tokens, "tokens", N, torch.int64, dev)
     if out is None:
-        out = torch.empty(N, D, dtype=weight.dtype if out_dtype is None else out_dtype, device=dev)
-        _used_on(stream, out)
-    elif out_dtype is not None and out_dtype != out.dtype:
-        raise TypeError("out_dtype disagrees with the given out")
-    n, d, ldo = _rows(out, "out", types)
-    if (n, d) != (N, D) or out.device != dev:
-        raise ValueError(f"out: {(n, d)} on {out.device}, expected {(N, D)} on {dev}")
-    st = L.ll_embed_forward(_ptr(weight), ldw, _code(weight.dtype), _ptr(tokens), N, D, V, int(v0),
-                            float(scale), _ptr(out), ldo, _code(out.dtype),
+        if out_dtype is None:
+            out_dtype = weight.dtype
+        elif out_dtype not in codes:
+            raise TypeError(f"out_dtype {out_dtype}, expected one of {tuple(codes)}")
+        out, ldo = _new((N, D), out_dtype, dev, stream), D
+    else:
+        if out_dtype is not None and out_dtype != out.dtype:
+            raise TypeError("out_dtype disagrees with the given out")
+        n, d, ldo = _rows(out, "out")
+        if n != N or d != D or out.device != dev:
+            raise ValueError(f"out: {(n, d)} on {out.device}, expected {(N, D)} on {dev}")
+    st = L.ll_embed_forward(weight.data_ptr(), ldw, codes[weight.dtype], tokens.data_ptr(), N, D,
+                            V, v0, scale, out.data_ptr(), ldo, codes[out.dtype],
                             _stream_of(dev, stream))
-    _check("ll_embed_forward", st)
+    if st:
+        raise LLError("ll_embed_forward", st)
     return out
 
 
@@ -669,30 +704,32 @@ def embed_backward(grad_out, tokens, V, *, scale=1.0, v0=0, dw_dtype=None, accum
     (tied weights: the grad_weight of `backward`)."""
     torch = _torch()
     L = load()
-    types = _float_types()
-    N, D, ldg = _rows(grad_out, "grad_out", types)
+    codes = _codes()
+    N, D, ldg = _rows(grad_out, "grad_out")
     V = int(V)
     dev = grad_out.device
-    _need(tokens, "tokens", (N,), torch.int64, dev)
+    _vector(tokens, "tokens", N, torch.int64, dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the table to add into (out)")
-        out = torch.empty(V, D, dtype=torch.float32 if dw_dtype is None else dw_dtype, device=dev)
-        _used_on(stream, out)
-    elif dw_dtype is not None and dw_dtype != out.dtype:
-        raise TypeError("dw_dtype disagrees with the given out")
-    v, d, ldw = _rows(out, "out", types)
-    if (v, d) != (V, D) or out.device != dev:
-        raise ValueError(f"out: {(v, d)} on {out.device}, expected {(V, D)} on {dev}")
-    if workspace is None:
-        workspace = _workspace(L.ll_embed_workspace_size(N, D, V), dev)
-        _used_on(stream, workspace)
-    _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
-    st = L.ll_embed_backward(_ptr(grad_out), ldg, _code(grad_out.dtype), _ptr(tokens), N, D, V,
-                             int(v0), float(scale), int(bool(accumulate)), _ptr(out), ldw,
-                             _code(out.dtype), _ptr(workspace), workspace.numel(),
+        if dw_dtype is None:
+            dw_dtype = torch.float32
+        elif dw_dtype not in codes:
+            raise TypeError(f"dw_dtype {dw_dtype}, expected one of {tuple(codes)}")
+        out, ldw = _new((V, D), dw_dtype, dev, stream), D
+    else:
+        if dw_dtype is not None and dw_dtype != out.dtype:
+            raise TypeError("dw_dtype disagrees with the given out")
+        v, d, ldw = _rows(out, "out")
+        if v != V or d != D or out.device != dev:
+            raise ValueError(f"out: {(v, d)} on {out.device}, expected {(V, D)} on {dev}")
+    workspace = _scratch(workspace, L.ll_embed_workspace_size(N, D, V), dev, stream)
+    st = L.ll_embed_backward(grad_out.data_ptr(), ldg, codes[grad_out.dtype], tokens.data_ptr(), N,
+                             D, V, v0, scale, 1 if accumulate else 0, out.data_ptr(), ldw,
+                             codes[out.dtype], workspace.data_ptr(), workspace.shape[0],
                              _stream_of(dev, stream))
-    _check("ll_embed_backward", st)
+    if st:
+        raise LLError("ll_embed_backward", st)
     return out
 
 
@@ -716,42 +753,44 @@ def policy_loss(logp, old_logp, advantages, *, ref_logp=None, mask=None, seq_off
     tokens (sequences) of this call."""
     torch = _torch()
     L = load()
-    N = logp.numel() if isinstance(logp, torch.Tensor) else 0
-    _need(logp, "logp", (N,), torch.float32)
-    dev = logp.device
-    _need(old_logp, "old_logp", (N,), torch.float32, dev)
-    _need(advantages, "advantages", (N,), torch.float32, dev)
+    f32 = torch.float32
+    if not isinstance(logp, torch.Tensor) or logp.dim() != 1:
+        raise TypeError("logp must be a 1-D torch.Tensor")
+    N, dev = logp.shape[0], logp.device
+    _vector(logp, "logp", N, f32, dev)
+    _vector(old_logp, "old_logp", N, f32, dev)
+    _vector(advantages, "advantages", N, f32, dev)
+    ref = msk = offs = None
+    B = 0
     if ref_logp is not None:
-        _need(ref_logp, "ref_logp", (N,), torch.float32, dev)
+        _vector(ref_logp, "ref_logp", N, f32, dev)
+        ref = ref_logp.data_ptr()
     if mask is not None:
         _need(mask, "mask", (N,), device=dev, dtypes=(torch.bool, torch.uint8))
-    B = 0
+        msk = mask.data_ptr()
     if seq_offsets is not None:
-        B = max(seq_offsets.numel() - 1, 0) if isinstance(seq_offsets, torch.Tensor) else 0
-        _need(seq_offsets, "seq_offsets", (B + 1,), torch.int64, dev)
-        if B == 0:
+        B = seq_offsets.numel() - 1 if isinstance(seq_offsets, torch.Tensor) else 0
+        _vector(seq_offsets, "seq_offsets", B + 1, torch.int64, dev)
+        if B < 1:
             raise ValueError("seq_offsets: at least two are needed")
-    if denominator is not None and not float(denominator) > 0:
+        offs = seq_offsets.data_ptr()
+    if denominator is None:
+        denominator = 0.0
+    elif not denominator > 0:
         raise ValueError("denominator must be > 0")
     if out is None:
-        stats = torch.empty(4, dtype=torch.float32, device=dev)
-        grad = torch.empty(N, dtype=torch.float32, device=dev)
-        _used_on(stream, stats, grad)
+        stats, grad = _new((4,), f32, dev, stream), _new((N,), f32, dev, stream)
     else:
         stats, grad = out
-    _need(stats, "stats", (4,), torch.float32, dev)
-    _need(grad, "grad_logp", (N,), torch.float32, dev)
-    if workspace is None:
-        workspace = _workspace(L.ll_policy_workspace_size(N, B), dev)
-        _used_on(stream, workspace)
-    _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
-    opt = PolicyOptions(float(clip_low), float(clip_high), float(kl_coef),
-                        0.0 if denominator is None else float(denominator))
-    st = L.ll_policy_loss(_ptr(logp), _ptr(old_logp), _ptr(ref_logp), _ptr(advantages),
-                          _ptr(mask), _ptr(seq_offsets), B, N, ctypes.byref(opt), _ptr(stats),
-                          _ptr(grad), _ptr(workspace), workspace.numel(),
-                          _stream_of(dev, stream))
-    _check("ll_policy_loss", st)
+        _vector(stats, "stats", 4, f32, dev)
+        _vector(grad, "grad_logp", N, f32, dev)
+    workspace = _scratch(workspace, L.ll_policy_workspace_size(N, B), dev, stream)
+    opt = PolicyOptions(clip_low, clip_high, kl_coef, denominator)
+    st = L.ll_policy_loss(logp.data_ptr(), old_logp.data_ptr(), ref, advantages.data_ptr(), msk,
+                          offs, B, N, ctypes.byref(opt), stats.data_ptr(), grad.data_ptr(),
+                          workspace.data_ptr(), workspace.shape[0], _stream_of(dev, stream))
+    if st:
+        raise LLError("ll_policy_loss", st)
     return stats, grad
 
 
@@ -762,26 +801,26 @@ class Tensor(ctypes.Structure):
 
 
 def _tensor_list(tensors):
-    """(ll_tensor array, device) of gradients that each fill their memory
-    without gaps, in any order of their dimensions."""
+    """(ll_tensor records as three 64-bit integers each, device) of gradients
+    that each fill their memory without gaps, in any order of their dimensions."""
     torch = _torch()
-    codes = DTYPE_CODES()
-    arr = (Tensor * len(tensors))()
-    dev = None
+    codes = _codes()
+    words = []
+    dev = where = None
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"tensor {i} must be a torch.Tensor")
-        if t.dtype not in codes:
+        code = codes.get(t.dtype)
+        if code is None:
             raise TypeError(f"tensor {i}: unsupported dtype {t.dtype}")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
+            dev, where = t.device, t.get_device()
+        elif t.get_device() != where:
             raise ValueError(f"tensor {i}: on {t.device}, expected {dev}")
         if not t.is_contiguous() and not _dense(t):
             raise ValueError(f"tensor {i}: its elements must fill their memory without gaps")
-        a = arr[i]
-        a.data, a.n, a.dtype = t.data_ptr(), t.numel(), codes[t.dtype]
-    return arr, dev
+        words += (t.data_ptr(), t.numel(), code)  # dtype and reserved = 0 share a word
+    return array.array("q", words), dev
 
 
 def _dense(t):
@@ -797,27 +836,26 @@ def _dense(t):
 def _norm_call(tensors, norm, workspace, stream):
     torch = _torch()
     L = load()
-    arr, dev = _tensor_list(tensors)
+    words, dev = _tensor_list(tensors)
     if dev is None:
         dev = norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        _used_on(stream, norm)
-    _need(norm, "norm", (), torch.float32, dev)
-    if workspace is None:
-        workspace = _workspace(L.ll_grad_norm_workspace_size(len(arr)), dev)
-        _used_on(stream, workspace)
-    _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
-    return L, arr, dev, norm, workspace
+        norm = _new((), torch.float32, dev, stream)
+    else:
+        _need(norm, "norm", (), torch.float32, dev)
+    count = len(words) // 3
+    workspace = _scratch(workspace, L.ll_grad_norm_workspace_size(count), dev, stream)
+    return L, words, count, dev, norm, workspace
 
 
 def grad_norm(tensors, *, out=None, workspace=None, stream=None):
     """The norm (0-d FP32) of a list of gradients taken as one vector.  Their
     dtypes may differ; each must fill its memory without gaps."""
-    L, arr, dev, out, workspace = _norm_call(tensors, out, workspace, stream)
-    st = L.ll_grad_norm(arr, len(arr), _ptr(out), _ptr(workspace), workspace.numel(),
-                        _stream_of(dev, stream))
-    _check("ll_grad_norm", st)
+    L, words, count, dev, out, workspace = _norm_call(tensors, out, workspace, stream)
+    st = L.ll_grad_norm(words.buffer_info()[0], count, out.data_ptr(), workspace.data_ptr(),
+                        workspace.shape[0], _stream_of(dev, stream))
+    if st:
+        raise LLError("ll_grad_norm", st)
     return out
 
 
@@ -826,8 +864,10 @@ def clip_grads(tensors, max_norm, *, norm=None, workspace=None, stream=None):
     and returns norm: that of the list, or a given one (0-d FP32 on the device:
     gradients sharded over ranks)."""
     given = norm is not None
-    L, arr, dev, norm, workspace = _norm_call(tensors, norm, workspace, stream)
-    st = L.ll_clip_grads(arr, len(arr), float(max_norm), int(given), _ptr(norm), _ptr(workspace),
-                         workspace.numel(), _stream_of(dev, stream))
-    _check("ll_clip_grads", st)
+    L, words, count, dev, norm, workspace = _norm_call(tensors, norm, workspace, stream)
+    st = L.ll_clip_grads(words.buffer_info()[0], count, max_norm, 1 if given else 0,
+                         norm.data_ptr(), workspace.data_ptr(), workspace.shape[0],
+                         _stream_of(dev, stream))
+    if st:
+        raise LLError("ll_clip_grads", st)
     return norm

@@ -1384,16 +1384,18 @@ int ll_clip_grads(const ll_tensor* tensors, int64_t count, float max_norm, int n
     if (!(max_norm > 0.f) || (norm_given & ~1) || !norm) return LL_ERR_INVALID_ARG;
     if (!aligned_to(norm, 4)) return LL_ERR_ALIGN;
     if (!norm_given) {
-        if ((st = ll_grad_norm(tensors, count, norm, workspace, ws_bytes, stream))) return st;
+        if (!workspace || ws_bytes < ll_grad_norm_workspace_size(count)) return LL_ERR_WORKSPACE;
+        if (!aligned_to(workspace, kAlign)) return LL_ERR_WORKSPACE;
     }
-    if (!any) return LL_OK;
+    if (!any && norm_given) return LL_OK;
     DeviceGuard guard(norm);
     if (guard.err) return guard.err;
     DevInfo dev;
     if ((st = device_info(guard.dev, &dev))) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Phase ph("grad_clip", s);
-    return cuda_status(launch_grad_clip(tensors, count, max_norm, norm, dev.num_sms, s));
+    return cuda_status(launch_grad_clip(tensors, count, max_norm, !norm_given, norm, workspace,
+                                        dev.num_sms, s));
 }
 
 int ll_check_status(void* stream) {

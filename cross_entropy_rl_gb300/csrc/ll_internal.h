@@ -329,22 +329,15 @@ size_t policy_ws_bytes(int64_t n_seqs);
 cudaError_t launch_policy_loss(const PolicyArgs& a, void* workspace, cudaStream_t s);
 
 // --- gradient norm and clipping (grad_kernels.cu) ------------------------------
-constexpr int kMaxTensors = 512;           // tensors of one launch
-constexpr int64_t kGradChunk = 16384;      // elements a block takes at a time
-constexpr int kGradBlocksPerSm = 8;
-constexpr int kGradMaxBlocks = 2048;       // most blocks, and so partial sums, of one launch
-struct GradList {
-    const void* data[kMaxTensors];
-    int64_t n[kMaxTensors];
-    int64_t first[kMaxTensors];  // number of the tensor's first chunk
-    uint8_t dtype[kMaxTensors];
-    int64_t chunk, chunks;
-    int count;
-};
+constexpr int kMaxTensors = 512;      // tensors of one launch
+constexpr int kGradMaxBlocks = 1024;  // most blocks, and so partial sums, of one launch
+// norm[0] = the norm of the list.
 cudaError_t launch_grad_norm(const ll_tensor* t, int64_t count, float* norm, void* ws,
                              int num_sms, cudaStream_t s);
-cudaError_t launch_grad_clip(const ll_tensor* t, int64_t count, float max_norm, const float* norm,
-                             int num_sms, cudaStream_t s);
+// The list scaled by min(1, max_norm / (norm + 1e-6)): by norm[0], or with
+// `compute` by the list's own, written to norm[0].
+cudaError_t launch_grad_clip(const ll_tensor* t, int64_t count, float max_norm, bool compute,
+                             float* norm, void* ws, int num_sms, cudaStream_t s);
 
 cudaError_t launch_unsatisfied_wait(int* flag, int* status, uint64_t wait_ns, cudaStream_t s);
 

@@ -195,36 +195,10 @@ __device__ __forceinline__ void count_sequences(const PolicyArgs& a, const Group
     flush();
 }
 
-// A sum held as hi + lo, |lo| at most half a step of hi: about 48 bits from
-// FP32 additions.  In FP64, of which an SM starts two operations a cycle, the
-// sums and weights kept that unit 77% busy and made most of the kernel's time
-// (48 us cold for a million tokens).  The _rn forms keep the compiler from fusing.
-struct Pair {
-    float hi, lo;
-};
-
-__device__ __forceinline__ float finite_or_0(float e, float of) {
-    return fabsf(of) < INFINITY ? e : 0.f;
-}
-
-__device__ __forceinline__ Pair add(Pair a, Pair b) {
-    const float s = __fadd_rn(a.hi, b.hi);
-    const float t = __fsub_rn(s, a.hi);
-    float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
-    e = finite_or_0(__fadd_rn(e, __fadd_rn(a.lo, b.lo)), s);
-    const float hi = __fadd_rn(s, e);
-    return {hi, finite_or_0(__fsub_rn(e, __fsub_rn(hi, s)), hi)};
-}
-
 // x times the weight w.
 __device__ __forceinline__ Pair times(float x, Pair w) {
     const float p = __fmul_rn(x, w.hi);
     return {p, finite_or_0(fmaf(x, w.lo, fmaf(x, w.hi, -p)), p)};
-}
-
-__device__ __forceinline__ Pair pair_of(double x) {
-    const float hi = static_cast<float>(x);
-    return {hi, static_cast<float>(x - hi)};
 }
 
 // one / c: an FP32 quotient and its remainder's.
@@ -232,13 +206,6 @@ __device__ __forceinline__ Pair per_token(Pair one, int c) {
     const float n = static_cast<float>(c), rest = static_cast<float>(c - static_cast<int>(n));
     const float q = __fdiv_rn(one.hi, n);
     return {q, __fdiv_rn(fmaf(-q, n, one.hi) + one.lo - q * rest, n)};
-}
-
-__device__ __forceinline__ Pair warp_sum(Pair x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        x = add(x, Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
-    return x;
 }
 
 // Gradients of a warp's groups; adds to s[0..2] the lane's share of the sums.
@@ -352,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) policy_count_kernel(const __grid_con
                                                                 PolicyWs* __restrict__ ws,
                                                                 int* __restrict__ seq_count) {
     const Groups g = grid_groups(a);
-    asm volatile("griddepcontrol.launch_dependents;");
+    launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) ws->done = 0;
     if (a.offs) {
         count_sequences(a, g, ws, seq_count);
@@ -376,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) policy_loss_kernel(const __grid_c
     loss_tokens(
         a,
         [&]() {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            wait_for_prerequisites();
             if (threadIdx.x < 32) {
                 unsigned long long n = 0;
                 if (a.offs) {
@@ -485,16 +452,8 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, void* workspace, cudaStream_
     const int64_t blocks = (a.N + kThreads - 1) / kThreads;
     const unsigned grid = static_cast<unsigned>(blocks < kPolicyBlocks ? blocks : kPolicyBlocks);
     policy_count_kernel<<<grid, kThreads, 0, s>>>(a, ws, seq_count);
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, policy_loss_kernel, a, ws, static_cast<const int*>(seq_count));
+    return launch_after(policy_loss_kernel, grid, kThreads, s, a, ws,
+                        static_cast<const int*>(seq_count));
 }
 
 }  // namespace ll
