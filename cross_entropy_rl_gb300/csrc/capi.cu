@@ -1221,6 +1221,15 @@ int check_tensors(const ll_tensor* t, int64_t count, bool apart, const void** an
         *any = t[i].data;
     }
     if (!apart || count < 2) return LL_OK;
+    uintptr_t end = 0;
+    bool ascending = true;  // as views of one buffer mostly are
+    for (int64_t i = 0; i < count && ascending; ++i) {
+        if (t[i].n == 0) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(t[i].data);
+        ascending = p >= end;
+        end = p + size_t(t[i].n) * esize(t[i].dtype);
+    }
+    if (ascending) return LL_OK;
     const ll_tensor** at = new (std::nothrow) const ll_tensor*[count];
     if (!at) return LL_ERR_INVALID_ARG;
     int64_t n = 0;

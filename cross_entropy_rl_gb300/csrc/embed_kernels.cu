@@ -90,19 +90,29 @@ bool rows16(const void* p, int64_t ld, size_t es) {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCtas = 8;        // CTAs of the sorting cluster
-constexpr int kSortBlock = 8;       // keys a lane loads at a time
-constexpr int kDigitBits = 9;       // most bits of a sorting pass
+constexpr int kSortCtas = 8;         // CTAs of the sorting cluster for many tokens
+constexpr int kDigitBits = 9;        // most bits of a sorting pass
 constexpr int kBins = 1 << kDigitBits;
-constexpr int kSortSmem = kSortWarps * kBins * 4;
-constexpr int kFillClusters = 32;  // clusters in all when rows are filled
-constexpr int kFillRows = kSortSmem * 8;  // vocabulary rows of one cluster's bitmap
-constexpr int kWindow = 16;         // sorted positions of a warp of the sums
+constexpr int kStaged = 4096;        // keys a CTA holds in shared memory
+constexpr int kWarpStaged = kStaged / kSortWarps;
+constexpr int kFillCtas = 256;       // CTAs in all when rows are filled
+constexpr int kFillRows = kSortWarps * kBins * 32;  // vocabulary rows of one bitmap (in the counts' place)
+#ifndef LL_W
+#define LL_W 16
+#define LL_K 32
+#endif
+constexpr int kWindow = LL_W;          // sorted positions of a warp of the sums
+
+// Shared memory of the sort: counts, keys (two buffers where one CTA sorts
+// alone), places of the keys among their equals.
+constexpr int sort_smem_bytes(int ctas) {
+    return kSortWarps * kBins * 4 + kStaged * 8 * (ctas == 1 ? 2 : 1) + kStaged * 2;
+}
 
 // Positions of a piece: few enough that a token of a third of a large batch is
 // spread over the device, and that at most 2048 pieces' partial sums are kept.
 __host__ __device__ inline int64_t piece_rows(int64_t N) {
-    int64_t k = 32;
+    int64_t k = LL_K;
     while ((N + k - 1) / k > 2048) k *= 2;
     return k;
 }
@@ -171,117 +181,150 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
     return s - x;
 }
 
-// Lanes whose digit (of `bits` bits, below 0: none) is this lane's.  One vote a
-// bit: match.any took ~75 cycles of the SM for each warp where most lanes
-// differ, and made half of the sort's time.
-__device__ __forceinline__ unsigned same_digit(int d, int bits) {
-    unsigned m = __ballot_sync(0xffffffffu, d >= 0);
-    if (d < 0) m = 0;
-    for (int b = 0; b < bits; ++b) {
-        const unsigned set = __ballot_sync(0xffffffffu, d >> b & 1);
-        m &= d >> b & 1 ? set : ~set;
+// m[r]: lanes whose digit d[r] (of `bits` bits, below 0: none) is this lane's.
+// One vote a bit, kRounds of them side by side: a vote and what hangs on it take
+// some 90 cycles, match.any 75 of the whole SM's where most lanes differ.
+constexpr int kRounds = 4;  // rounds of 32 keys of a warp at a time
+__device__ __forceinline__ void same_digits(const int (&d)[kRounds], int bits,
+                                            unsigned (&m)[kRounds]) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const unsigned any = __ballot_sync(0xffffffffu, d[r] >= 0);
+        m[r] = d[r] >= 0 ? any : 0;
     }
-    return m;
+#pragma unroll 1
+    for (int b = 0; b < bits; ++b)
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const unsigned set = __ballot_sync(0xffffffffu, d[r] >> b & 1);
+            m[r] &= d[r] >> b & 1 ? set : ~set;
+        }
 }
 
-// The run of keys [beg, end) of warp `me` of `warps`, of M in all.
-struct Run {
-    int64_t beg, end;
-    bool kept;  // one block of kSortBlock keys a lane: it stays in registers
-    __device__ Run(int64_t M, int64_t me, int64_t warps) {
-        const int64_t per = ((M + 31) / 32 + warps - 1) / warps * 32;
-        beg = me * per < M ? me * per : M;
-        end = beg + per < M ? beg + per : M;
-        kept = per <= 32 * kSortBlock;
-    }
-};
-
-// Least-significant-digit radix sort by one cluster, stable, so that the
-// positions of a token stay ascending.  Each warp owns a run of the keys; a
+// Least-significant-digit radix sort by one CTA or one cluster, stable, so that
+// the positions of a token stay ascending.  Each warp owns a run of the keys; a
 // pass counts the run's digits (one lane adds for all of its digit), scans the
 // counts over warps, CTAs and digits, and writes each key to its place.  Tokens
-// outside the table drop out in the first pass.
+// outside the table drop out in the first pass.  Runs of up to kWarpStaged keys
+// are staged in shared memory.  The loops are kept short: the sort is some ten
+// thousand cycles long and its instructions are fetched cold (eight rounds
+// unrolled, counting 300 tokens took 3.2k cycles instead of 0.9k).
+template <int CTAS>
 __device__ void sort_tokens(const SortArgs& a) {
+    typedef unsigned long long Key;
+    constexpr Key kNone = ~0ull;
     int* hist = reinterpret_cast<int*>(sort_smem);  // [kSortWarps][bins]
+    Key* keys = reinterpret_cast<Key*>(sort_smem + kSortWarps * kBins * 4);
+    uint16_t* places = reinterpret_cast<uint16_t*>(keys + kStaged * (CTAS == 1 ? 2 : 1));
     __shared__ int total[kBins], base[kBins], scan[kSortWarps], grand;
+    __shared__ int last_head[kSortWarps];
     static_assert(kBins == kSortThreads, "a thread per digit");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_ctarank();
-    const int64_t warps = kSortCtas * kSortWarps, me = rank * kSortWarps + warp;
+    const uint32_t rank = CTAS == 1 ? 0 : cluster_ctarank();
+    constexpr int kWarps = CTAS * kSortWarps;
+    const int me = rank * kSortWarps + warp;
     const unsigned lt = (1u << lane) - 1;
+    auto all_ctas = [&]() {
+        __syncthreads();
+        if (CTAS > 1) cluster_barrier();
+    };
 
-    if (rank == 0 && tid == 0) a.p.head->longs = 0;  // ahead of cluster barriers
+    if (rank == 0 && tid == 0) a.p.head->longs = 0;  // ahead of barriers of all CTAs
 
-    int64_t M = a.N;
+    int64_t M = a.N, beg, end;
+    bool staged;
+    Key* mine;  // the warp's staged keys
+    auto set_run = [&]() {
+        const int64_t per = ((M + 31) / 32 + kWarps - 1) / kWarps * 32;
+        beg = me * per < M ? me * per : M;
+        end = beg + per < M ? beg + per : M;
+        staged = per <= kWarpStaged;  // always, where one CTA sorts alone
+        mine = keys + (CTAS == 1 ? beg : int64_t(warp) * kWarpStaged);
+    };
+    // Sorted keys of the passes, alternately in two buffers; ahead of the first,
+    // keys made of the tokens.
+    const Key* src = nullptr;
+    Key* dst = CTAS == 1 ? keys + kStaged : a.p.buf0;
+    auto key_of = [&](int64_t i, int64_t y) -> Key {
+        const int64_t v = y - a.v0;
+        if (y < a.v0 || v >= a.V) return kNone;
+        return static_cast<Key>(v) << 32 | static_cast<unsigned>(i);
+    };
+    auto source = [&](int64_t i) {
+        return src ? __ldcg(src + i) : key_of(i, a.tokens[i]);
+    };
+    auto stage = [&]() {
+        if (beg >= end) return;
+        int64_t x[kWarpStaged / 32];
+        const int64_t* from = src ? reinterpret_cast<const int64_t*>(src) : a.tokens;
+#pragma unroll
+        for (int q = 0; q < kWarpStaged / 32; ++q) {
+            const int64_t i = beg + q * 32 + lane;
+            x[q] = __ldcg(from + (i < end ? i : end - 1));
+        }
+#pragma unroll
+        for (int q = 0; q < kWarpStaged / 32; ++q) {
+            const int64_t i = beg + q * 32 + lane;
+            if (i < end) mine[q * 32 + lane] = src ? static_cast<Key>(x[q]) : key_of(i, x[q]);
+        }
+    };
+    // Keys of kRounds rounds from i on, i the lane's first.
+    auto block = [&](int64_t i, Key (&k)[kRounds]) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int64_t at = i + r * 32;
+            k[r] = at >= end ? kNone : staged ? mine[at - beg] : source(at);
+        }
+    };
+
     int shift = 0;
     for (int pass = 0; pass < a.passes; ++pass) {
         const int db = (a.bits - shift + (a.passes - pass) - 1) / (a.passes - pass);
         const int bins = 1 << db;
-        const unsigned long long* src = (pass & 1) ? a.p.buf0 : a.p.buf1;
-        unsigned long long* dst = (pass & 1) ? a.p.buf1 : a.p.buf0;
-        const Run run(M, me, warps);
-        unsigned long long k[kSortBlock];
-        int d[kSortBlock];  // digit; of a kept run, with the place among its equals above
-        auto fetch = [&](int64_t i0) {
-#pragma unroll
-            for (int r = 0; r < kSortBlock; ++r) {
-                const int64_t i = i0 + r * 32 + lane;
-                d[r] = -1;
-                if (i >= run.end) continue;
-                if (pass > 0) {
-                    k[r] = __ldcg(src + i);
-                    d[r] = 0;
-                } else {
-                    const int64_t y = a.tokens[i];
-                    const int64_t v = y - a.v0;
-                    k[r] = (static_cast<unsigned long long>(v) << 32) | static_cast<unsigned>(i);
-                    if (y >= a.v0 && v < a.V) d[r] = 0;
-                }
-            }
-        };
-        auto digits = [&]() {
-#pragma unroll
-            for (int r = 0; r < kSortBlock; ++r)
-                if (d[r] == 0) d[r] = static_cast<int>(k[r] >> (32 + shift)) & (bins - 1);
-        };
-        if (run.kept) fetch(run.beg);  // on its way while the counts are cleared
+        set_run();
+        if (staged && (CTAS > 1 || pass == 0)) stage();
         for (int i = tid; i < kSortWarps * bins; i += kSortThreads) hist[i] = 0;
         __syncthreads();
-        int* mine = hist + warp * bins;
-        for (int64_t i0 = run.beg; i0 < run.end; i0 += 32 * kSortBlock) {
-            if (!run.kept) fetch(i0);
-            digits();
+        int* count = hist + warp * bins;
+        auto digit = [&](Key k) { return k == kNone ? -1 : static_cast<int>(k >> (32 + shift)) & (bins - 1); };
+        const int place0 = static_cast<int>((mine - keys) % kStaged - beg);
+#pragma unroll 1
+        for (int64_t i = beg + lane; i - lane < end; i += 32 * kRounds) {
+            Key k[kRounds];
+            int d[kRounds];
+            unsigned peers[kRounds];
+            block(i, k);
 #pragma unroll
-            for (int r = 0; r < kSortBlock; ++r) {
-                const unsigned peers = same_digit(d[r], db);
-                const int had = d[r] >= 0 ? mine[d[r]] : 0;
+            for (int r = 0; r < kRounds; ++r) d[r] = digit(k[r]);
+            same_digits(d, db, peers);
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r) {
+                const int had = d[r] >= 0 ? count[d[r]] : 0;
                 __syncwarp();
                 if (d[r] >= 0) {
-                    if ((peers & lt) == 0) mine[d[r]] = had + __popc(peers);
-                    if (run.kept) d[r] |= (had + __popc(peers & lt)) << kDigitBits;
+                    if ((peers[r] & lt) == 0) count[d[r]] = had + __popc(peers[r]);
+                    if (staged) places[place0 + i + r * 32] = had + __popc(peers[r] & lt);
                 }
                 __syncwarp();
             }
         }
         __syncthreads();
         if (tid < bins) {  // counts of the warps below, and of the CTA
-            int c[kSortWarps], sum = 0;
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w * bins + tid];
+            int sum = 0;
 #pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
+                const int c = hist[w * bins + tid];
                 hist[w * bins + tid] = sum;
-                sum += c[w];
+                sum += c;
             }
             total[tid] = sum;
         }
-        __syncthreads();
-        cluster_barrier();
+        all_ctas();
         int before = 0, all = 0;
         if (tid < bins) {
 #pragma unroll
-            for (uint32_t r = 0; r < kSortCtas; ++r) {
-                const int c = ld_cluster(total + tid, r);
+            for (uint32_t r = 0; r < CTAS; ++r) {
+                const int c = CTAS == 1 ? total[tid] : ld_cluster(total + tid, r);
                 if (r < rank) before += c;
                 all += c;
             }
@@ -289,111 +332,132 @@ __device__ void sort_tokens(const SortArgs& a) {
         const int low = warp_scan(all, lane);  // digits below, within 32
         if (lane == 31) scan[warp] = low + all;
         __syncthreads();
-        if (warp == 0) {
-            const int c = lane < kSortWarps ? scan[lane] : 0;
-            const int s = warp_scan(c, lane);
-            if (lane < kSortWarps) scan[lane] = s;
-            if (lane == 31) grand = s + c;
+        int under = 0, sum = 0;  // digits of the warps below
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            if (w < warp) under += scan[w];
+            sum += scan[w];
         }
+        if (tid < bins) base[tid] = under + low + before;
+        if (tid == 0) grand = sum;
         __syncthreads();
-        if (tid < bins) base[tid] = scan[warp] + low + before;
-        M = pass == 0 ? grand : M;
-        __syncthreads();
-        for (int64_t i0 = run.beg; i0 < run.end; i0 += 32 * kSortBlock) {
-            if (run.kept) {
+#pragma unroll 1
+        for (int64_t i = beg + lane; i - lane < end; i += 32 * kRounds) {
+            Key k[kRounds];
+            int d[kRounds], at[kRounds];
+            block(i, k);
 #pragma unroll
-                for (int r = 0; r < kSortBlock; ++r)
-                    if (d[r] >= 0) {
-                        const int b = d[r] & (kBins - 1);
-                        dst[mine[b] + base[b] + (d[r] >> kDigitBits)] = k[r];
-                    }
-                break;
-            }
-            fetch(i0);
-            digits();
+            for (int r = 0; r < kRounds; ++r) d[r] = digit(k[r]);
+            if (staged) {
 #pragma unroll
-            for (int r = 0; r < kSortBlock; ++r) {
-                const unsigned peers = same_digit(d[r], db);
-                const int had = d[r] >= 0 ? mine[d[r]] : 0;
-                __syncwarp();
-                if (d[r] >= 0) {
-                    if ((peers & lt) == 0) mine[d[r]] = had + __popc(peers);
-                    dst[had + base[d[r]] + __popc(peers & lt)] = k[r];
+                for (int r = 0; r < kRounds; ++r)
+                    at[r] = d[r] >= 0 ? count[d[r]] + base[d[r]] + places[place0 + i + r * 32] : 0;
+            } else {
+                unsigned peers[kRounds];
+                same_digits(d, db, peers);
+#pragma unroll
+                for (int r = 0; r < kRounds; ++r) {
+                    const int had = d[r] >= 0 ? count[d[r]] : 0;
+                    __syncwarp();
+                    if (d[r] >= 0 && (peers[r] & lt) == 0) count[d[r]] = had + __popc(peers[r]);
+                    __syncwarp();
+                    at[r] = d[r] >= 0 ? had + base[d[r]] + __popc(peers[r] & lt) : 0;
                 }
-                __syncwarp();
             }
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r)
+                if (d[r] >= 0) dst[at[r]] = k[r];
         }
         shift += db;
-        __syncthreads();
-        cluster_barrier();  // every key of the pass is in its place
+        if (pass == 0) M = grand;
+        if (CTAS == 1) {
+            Key* t = keys;
+            keys = dst;
+            dst = t;
+        } else {
+            src = dst;
+            dst = dst == a.p.buf0 ? a.p.buf1 : a.p.buf0;
+        }
+        all_ctas();  // every key of the pass is in its place
     }
 
     // The entries with their units' ends.  All that a warp needs from the runs
     // ahead of its own is where the last token started.
-    __shared__ int last_head[kSortWarps];
-    const unsigned long long* key = (a.passes & 1) ? a.p.buf0 : a.p.buf1;
-    const Run run(M, me, warps);
-    unsigned long long k[kSortBlock];
-    unsigned heads[kSortBlock];  // lanes whose key starts a token
-    unsigned after;              // row of the key after the block
-    auto fetch = [&](int64_t i0) {
-        unsigned before = ~0u;  // row of the key ahead of the block
-        after = ~0u;
+    set_run();
+    if (CTAS > 1 && staged) stage();
+    __syncwarp();
+    auto row_at = [&](int64_t i) -> unsigned {
+        if (i < 0 || i >= M) return ~0u;
+        const Key k = CTAS == 1 ? keys[i] : __ldcg(src + i);
+        return static_cast<unsigned>(k >> 32);
+    };
+    const unsigned row_before = row_at(beg - 1), row_after = row_at(end);
+    // Lanes of each round that start a token; the row ahead of the block goes in
+    // and the block's last comes out of `prev`.
+    auto heads_of = [&](const Key (&k)[kRounds], int64_t i, unsigned& prev, unsigned (&heads)[kRounds]) {
 #pragma unroll
-        for (int r = 0; r < kSortBlock; ++r) {
-            const int64_t i = i0 + r * 32 + lane;
-            k[r] = i < M ? __ldcg(key + i) : ~0ull;
-        }
-        if (i0 > 0) before = static_cast<unsigned>(__ldcg(key + i0 - 1) >> 32);
-        if (i0 + 32 * kSortBlock < M)
-            after = static_cast<unsigned>(__ldcg(key + i0 + 32 * kSortBlock) >> 32);
-#pragma unroll
-        for (int r = 0; r < kSortBlock; ++r) {
+        for (int r = 0; r < kRounds; ++r) {
             const unsigned row = static_cast<unsigned>(k[r] >> 32);
             const unsigned up = __shfl_up_sync(0xffffffffu, row, 1);
-            const unsigned prev = lane == 0 ? before : up;
-            heads[r] = __ballot_sync(0xffffffffu, i0 + r * 32 + lane < run.end && row != prev);
-            before = __shfl_sync(0xffffffffu, row, 31);
+            heads[r] = __ballot_sync(0xffffffffu, i + r * 32 < end && row != (lane == 0 ? prev : up));
+            prev = __shfl_sync(0xffffffffu, row, 31);
         }
     };
     int last = -1;
-    for (int64_t i0 = run.beg; i0 < run.end; i0 += 32 * kSortBlock) {
-        fetch(i0);
+    unsigned prev = row_before;
+#pragma unroll 1
+    for (int64_t i = beg + lane; i - lane < end; i += 32 * kRounds) {
+        Key k[kRounds];
+        unsigned heads[kRounds];
+        block(i, k);
+        heads_of(k, i, prev, heads);
 #pragma unroll
-        for (int r = 0; r < kSortBlock; ++r)
-            if (heads[r]) last = static_cast<int>(i0) + r * 32 + 31 - __clz(heads[r]);
+        for (int r = 0; r < kRounds; ++r)
+            if (heads[r]) last = static_cast<int>(i) - lane + r * 32 + 31 - __clz(heads[r]);
     }
     if (lane == 0) last_head[warp] = last;
-    __syncthreads();
-    cluster_barrier();
+    all_ctas();
     int head = -1;  // of the token that the run may start inside
-    static_assert(kSortCtas * kSortWarps % 32 == 0, "whole warps");
 #pragma unroll
-    for (int r = 0; r < kSortCtas * kSortWarps / 32; ++r) {
+    for (int r = 0; r < (kWarps + 31) / 32; ++r) {
         const int w = r * 32 + lane;
-        const int h = ld_cluster(last_head + w % kSortWarps, w / kSortWarps);
-        if (w < me) head = max(head, h);
+        if (w < me) {
+            const int h = CTAS == 1 ? last_head[w % kSortWarps]
+                                    : ld_cluster(last_head + w % kSortWarps, w / kSortWarps);
+            head = max(head, h);
+        }
     }
     head = __reduce_max_sync(0xffffffffu, head);
-    for (int64_t i0 = run.beg; i0 < run.end; i0 += 32 * kSortBlock) {
-        if (!run.kept) fetch(i0);
+    prev = row_before;
+    const int mask = a.K - 1;  // K is a power of two
+#pragma unroll 1
+    for (int64_t i0 = beg + lane; i0 - lane < end; i0 += 32 * kRounds) {
+        Key k[kRounds];
+        unsigned heads[kRounds];
+        block(i0, k);
+        heads_of(k, i0, prev, heads);
+        // the row after the block
+        const int64_t i1 = i0 - lane + 32 * kRounds;
+        unsigned beyond = row_after;
+        if (i1 < end)
+            beyond = static_cast<unsigned>((staged ? mine[i1 - beg] : source(i1)) >> 32);
 #pragma unroll
-        for (int r = 0; r < kSortBlock; ++r) {
-            const int b = static_cast<int>(i0) + r * 32, i = b + lane;
+        for (int r = 0; r < kRounds; ++r) {
+            const int i = static_cast<int>(i0) + r * 32, b = i - lane;
             const unsigned row = static_cast<unsigned>(k[r] >> 32);
             const unsigned down = __shfl_down_sync(0xffffffffu, row, 1);
-            const unsigned first = r + 1 < kSortBlock
-                                       ? __shfl_sync(0xffffffffu, static_cast<unsigned>(k[r + 1 < kSortBlock ? r + 1 : r] >> 32), 0)
-                                       : after;
-            const unsigned behind = lane == 31 ? first : down;  // ~0 past the last key
+            const unsigned first =
+                r + 1 < kRounds ? __shfl_sync(0xffffffffu, static_cast<unsigned>(k[(r + 1) % kRounds] >> 32), 0)
+                                : beyond;
             const unsigned upto = heads[r] & (lt | (1u << lane));
             const int h = upto ? b + 31 - __clz(upto) : head;
-            if (i < run.end) {
-                const int in = (i - h) % a.K;  // place in its unit
-                const bool token_ends = row != behind;
-                const bool end = token_ends || in == a.K - 1;
-                const bool more = end && (i - h >= a.K || !token_ends);
-                a.p.entries[i] = Entry{static_cast<unsigned>(k[r]) | (end ? kTop : 0u),
+            if (i < end) {
+                const unsigned next = i + 1 == end ? row_after : lane == 31 ? first : down;
+                const int in = (i - h) & mask;  // place in its unit
+                const bool token_ends = row != next;
+                const bool unit_ends = token_ends || in == mask;
+                const bool more = unit_ends && (i - h >= a.K || !token_ends);
+                a.p.entries[i] = Entry{static_cast<unsigned>(k[r]) | (unit_ends ? kTop : 0u),
                                        row | (more ? kTop : 0u)};
                 if (i % kWindow == 0) a.p.windows[i / kWindow] = i - in;
                 if (token_ends && i - h >= a.K)
@@ -407,8 +471,7 @@ __device__ void sort_tokens(const SortArgs& a) {
         a.p.head->valid = static_cast<int>(M);
         a.p.windows[(M + kWindow - 1) / kWindow] = static_cast<int>(M);
     }
-    __syncthreads();
-    cluster_barrier();  // no CTA leaves while another reads its shared memory
+    all_ctas();  // no CTA leaves while another reads its shared memory
 }
 
 // Rows of no token set to +0, by the clusters that do not sort: each takes a
@@ -450,12 +513,12 @@ __device__ void fill_rows(const SortArgs& a, int64_t cluster, int64_t clusters) 
     }
 }
 
+template <int CTAS>
 __global__ void __launch_bounds__(kSortThreads, 2) embed_sort_kernel(const __grid_constant__ SortArgs a) {
-    const int64_t cluster = blockIdx.x / cluster_ctas(), clusters = gridDim.x / cluster_ctas();
-    if (cluster == 0)
-        sort_tokens(a);
+    if (blockIdx.x < CTAS)
+        sort_tokens<CTAS>(a);
     else
-        fill_rows(a, cluster - 1, clusters - 1);
+        fill_rows(a, blockIdx.x / CTAS - 1, gridDim.x / CTAS - 1);
 }
 
 struct GradArgs {
@@ -485,13 +548,13 @@ __global__ void __launch_bounds__(32 * kGradWarps, LL_GC) embed_grad_kernel(
     const int lane = threadIdx.x & 31;
     const int M = a.p.head->valid;
     const int64_t items = int64_t((M + kWindow - 1) / kWindow) * a.tiles;
-    for (int64_t it = blockIdx.x * int64_t(kGradWarps) + (threadIdx.x >> 5); it < items;
-         it += int64_t(gridDim.x) * kGradWarps) {
-        const int64_t w = it / a.tiles;
-        const int64_t c0 = ((it - w * a.tiles) * C * 32 + lane) * E;
+    const int64_t it0 = blockIdx.x * int64_t(kGradWarps) + (threadIdx.x >> 5);
+    for (int64_t it = it0; it < items; it += int64_t(gridDim.x) * kGradWarps) {
+        const int64_t c0 = (it % a.tiles * C * 32 + lane) * E;
         bool has[C];
 #pragma unroll
         for (int k = 0; k < C; ++k) has[k] = c0 + k * 32 * E < a.D;
+        const int64_t w = it / a.tiles;
         const int p0 = a.p.windows[w], p1 = a.p.windows[w + 1];
         int start = p0;  // of the unit
         float acc[C][E];
@@ -500,29 +563,29 @@ __global__ void __launch_bounds__(32 * kGradWarps, LL_GC) embed_grad_kernel(
 #pragma unroll
             for (int j = 0; j < E; ++j) acc[k][j] = 0.f;
         for (int b = p0; b < p1; b += 32) {
-            Entry mine{0, 0};
-            if (b + lane < p1) mine = a.p.entries[b + lane];
+            const Entry mine = b + lane < p1 ? a.p.entries[b + lane] : Entry{0, 0};
             const int n = p1 - b < 32 ? p1 - b : 32;
 #pragma unroll 1
             for (int r = 0; r < n; r += R) {
                 Pack<TI, E> x[R][C];
-                Pack<TO, E> old[R][C];
-                const TI* src[R];
-                Entry e[R];
+                Pack<TO, E> old[ADD ? R : 1][C];
+                auto entry = [&](int q) {
+                    return Entry{__shfl_sync(0xffffffffu, mine.pos, (r + q) & 31),
+                                 __shfl_sync(0xffffffffu, mine.row, (r + q) & 31)};
+                };
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
-                    e[q].pos = __shfl_sync(0xffffffffu, mine.pos, (r + q) & 31);
-                    e[q].row = __shfl_sync(0xffffffffu, mine.row, (r + q) & 31);
+                    const Entry e = entry(q);
                     if (r + q < n) {
-                        src[q] = g + int64_t(e[q].pos & ~kTop) * a.ldg + c0;
+                        const TI* src = g + int64_t(e.pos & ~kTop) * a.ldg + c0;
 #pragma unroll
                         for (int k = 0; k < C; ++k)
-                            if (has[k]) x[q][k].load(src[q] + k * 32 * E);
-                        if (ADD && (e[q].pos & kTop) && !(e[q].row & kTop)) {
-                            const TO* row = dW + int64_t(e[q].row) * a.ldw + c0;
+                            if (has[k]) x[q][k].load(src + k * 32 * E);
+                        if (ADD && (e.pos & kTop) && !(e.row & kTop)) {
+                            const TO* row = dW + int64_t(e.row) * a.ldw + c0;
 #pragma unroll
                             for (int k = 0; k < C; ++k)
-                                if (has[k]) old[q][k].load(row + k * 32 * E);
+                                if (has[k]) old[ADD ? q : 0][k].load(row + k * 32 * E);
                         }
                     }
                 }
@@ -533,16 +596,17 @@ __global__ void __launch_bounds__(32 * kGradWarps, LL_GC) embed_grad_kernel(
                     for (int k = 0; k < C; ++k)
 #pragma unroll
                         for (int j = 0; j < E; ++j) acc[k][j] += Elem<TI>::to_f(x[q][k].e[j]);
-                    if (!(e[q].pos & kTop)) continue;
-                    if (!(e[q].row & kTop)) {
-                        TO* row = dW + int64_t(e[q].row) * a.ldw + c0;
+                    const Entry e = entry(q);
+                    if (!(e.pos & kTop)) continue;
+                    if (!(e.row & kTop)) {
+                        TO* row = dW + int64_t(e.row) * a.ldw + c0;
 #pragma unroll
                         for (int k = 0; k < C; ++k) {
                             Pack<TO, E> y;
 #pragma unroll
                             for (int j = 0; j < E; ++j)
                                 y.e[j] = grad_value<TO>(a.scale * acc[k][j],
-                                                        ADD ? Elem<TO>::to_f(old[q][k].e[j]) : 0.f);
+                                                        ADD ? Elem<TO>::to_f(old[ADD ? q : 0][k].e[j]) : 0.f);
                             if (has[k]) y.store(row + k * 32 * E);
                         }
                     } else {
@@ -727,19 +791,25 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, int 
     a.row_bytes = e.D * es;
     a.pitch = e.ld_table * es;
 
+    note_launches(1);
+    const int ctas = e.N <= kStaged ? 1 : kSortCtas;
+    auto* kernel = ctas == 1 ? embed_sort_kernel<1> : embed_sort_kernel<kSortCtas>;
+    const int smem = sort_smem_bytes(ctas);
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = kSortCtas;
+    at.val.clusterDim.x = ctas;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(accumulate ? kSortCtas : kSortCtas * kFillClusters);
+    cfg.gridDim = dim3(accumulate ? ctas : kFillCtas);
     cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = kSortSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    note_launches(1);
-    return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_embed_bwd(const EmbedArgs& e, int accumulate, void* ws, int num_sms,

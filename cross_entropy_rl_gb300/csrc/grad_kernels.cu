@@ -3,11 +3,11 @@
 //   norm = sqrt(sum_i sum_j g_ij^2),  g *= min(1, max_norm / (norm + 1e-6))
 //
 // Both are bound by HBM: the norm reads every element once, the clipping reads
-// and writes every element once.  A list is cut into chunks of a fixed number
-// of elements that blocks take in turn; the table of the tensors travels in the
-// launch parameters, so a list costs one launch per kMaxTensors.  The clipping
-// takes the chunks in descending order: what the norm read last is still in L2.
-// A short list is one launch of one cluster that does both.
+// and writes every element once.  The list is laid end to end in chunks, each
+// block takes an equal run of them and streams it; the table of the tensors
+// travels in the launch parameters, so a list costs one launch per kMaxTensors.
+// The clipping goes through each run backwards: what the norm read last is still
+// in L2.  A short list is one launch of one cluster that does both.
 #include <math.h>
 
 #include "ll_device.cuh"
@@ -16,11 +16,17 @@ namespace ll {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kBlocksPerSm = 4;
-constexpr int kChunk = 32768;       // elements of a chunk
+// Measured on 1.97 GB (norm) and 0.76 GB (norm + clipping), us: 2 blocks an SM of
+// 8 loads 285 / 369, of 4 loads 289 / 370, 3 of 4 loads 351 / 387, 4 of 8 loads
+// (spilled) 612 / 548.
+constexpr int kBlocksPerSm = 2;
+constexpr int kUnroll = 8;          // 16-byte loads of a thread in flight
+constexpr int kChunk = 16384;       // bytes of a chunk: what the blocks' shares may differ by
 constexpr int kSmallCtas = 8;       // CTAs of the one-launch path's cluster
-constexpr int kSmallChunk = 4096;
-constexpr int64_t kSmallBytes = int64_t(4) << 20;  // most bytes of the one-launch path
+// Most bytes of the one-launch path: 128 KB in 1 / 40 tensors take 4.2 / 7.0 us in
+// one launch and 5.0 / 5.8 in three, 512 KB 4.3 / 8.6 and 6.0 / 6.1, 1 MB 4.8 / 13.3
+// and 6.2 / 6.6; the two launches saved are 7 us of the host's time.
+constexpr int64_t kSmallBytes = 512 << 10;
 
 // The tensors of a launch, up to N of them.
 template <int N>
@@ -29,85 +35,116 @@ struct GradList {
     int64_t n[N];
     int64_t first[N];  // number of the tensor's first chunk
     int64_t chunks;
-    int chunk, count;
+    int count;
     uint8_t dtype[N];
 };
 constexpr int kFewTensors = 64;  // a launch with a short table costs the host less
 
-// The elements [lo, hi) of one tensor that a chunk covers: the first chunk also
-// takes the elements ahead of the first 16-byte boundary, so that every other
-// chunk starts on one.
-struct Range {
-    int tensor;
-    int64_t lo, body, hi;  // [lo, body) lie ahead of the boundary
-};
-
-template <int N>
-__device__ __forceinline__ Range chunk_range(const GradList<N>& L, int64_t chunk) {
-    int a = 0, b = L.count;  // last tensor whose first chunk is <= chunk
-    while (b - a > 1) {
-        const int m = (a + b) >> 1;
-        if (L.first[m] <= chunk)
-            a = m;
-        else
-            b = m;
-    }
-    Range r;
-    r.tensor = a;
-    const int es = L.dtype[a] == LL_F32 ? 4 : 2;
-    const int64_t n = L.n[a];
-    int64_t head = ((16 - (reinterpret_cast<uintptr_t>(L.data[a]) & 15)) & 15) / es;
-    if (head > n) head = n;
-    const int64_t k = chunk - L.first[a];
-    r.body = head + k * L.chunk;
-    r.lo = k == 0 ? 0 : r.body;
-    r.hi = r.body + L.chunk < n ? r.body + L.chunk : n;
-    return r;
+// Elements ahead of a tensor's first 16-byte boundary.
+__host__ __device__ __forceinline__ int64_t head_of(const void* data, int64_t n, int es) {
+    const int64_t h = ((16 - (reinterpret_cast<uintptr_t>(data) & 15)) & 15) / es;
+    return h < n ? h : n;
 }
 
-// A thread's sum of squares: FP32 sums of one chunk's share (at most 72 terms),
-// added as a pair while every chunk's largest element lies in [2^-50, 2^55],
-// where neither the squares nor their sums leave the FP32 range nor lose what
-// matters; other chunks are squared again in 64 bits.
+// The elements [lo, hi) of a tensor; from `body` on they start on a 16-byte
+// boundary.
+struct Range {
+    int64_t lo, body, hi;
+};
+
+// Calls f(tensor, range) for the parts of the list's chunks [c0, c1) that lie in
+// one tensor each.  A tensor's first chunk also takes what lies ahead of its
+// first 16-byte boundary, so that the others start on one.
+template <int N, typename F>
+__device__ __forceinline__ void each_part(const GradList<N>& L, int64_t c0, int64_t c1,
+                                          bool backwards, const F& f) {
+    if (c0 >= c1) return;
+    auto tensor_of = [&](int64_t chunk) {  // the last whose first chunk is <= chunk
+        int a = 0, b = L.count;
+        while (b - a > 1) {
+            const int m = (a + b) >> 1;
+            if (L.first[m] <= chunk)
+                a = m;
+            else
+                b = m;
+        }
+        return a;
+    };
+    int a = tensor_of(backwards ? c1 - 1 : c0);
+    while (c0 < c1) {
+        const int64_t t0 = L.first[a], t1 = a + 1 < L.count ? L.first[a + 1] : L.chunks;
+        const int64_t p0 = c0 > t0 ? c0 : t0, p1 = c1 < t1 ? c1 : t1;
+        const int es = L.dtype[a] == LL_F32 ? 4 : 2;
+        const int64_t n = L.n[a], head = head_of(L.data[a], n, es), size = kChunk / es;
+        Range r;
+        r.body = head + (p0 - t0) * size;
+        r.lo = p0 == t0 ? 0 : r.body;
+        r.hi = head + (p1 - t0) * size < n ? head + (p1 - t0) * size : n;
+        f(a, r);
+        if (backwards)
+            c1 = p0, --a;
+        else
+            c0 = p1, ++a;
+    }
+}
+
+// A thread's sum of squares: FP32 sums of at most kUnroll packs, added as a pair
+// while their largest element lies in [2^-50, 2^55], where neither the squares
+// nor their sums leave the FP32 range nor lose what matters; others are squared
+// in 64 bits.
 struct Squares {
     Pair sum = {0.f, 0.f};
     double wide = 0;
     bool used_wide = false;
+
+    template <int K>
+    __device__ __forceinline__ void add_all(const float (&x)[K]) {
+        float s = 0.f, big = 0.f;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            s = fmaf(x[i], x[i], s);
+            big = fmaxf(big, fabsf(x[i]));  // a NaN is in s
+        }
+        if (big == 0.f || (big >= 0x1p-50f && big <= 0x1p55f)) {
+            sum = add(sum, Pair{s, 0.f});
+        } else {
+            used_wide = true;
+            for (int i = 0; i < K; ++i) wide += static_cast<double>(x[i]) * x[i];
+        }
+    }
 };
 
 template <typename T>
-__device__ void add_squares(const T* __restrict__ p, const Range& r, Squares& q) {
+__device__ __forceinline__ void add_squares(const T* __restrict__ p, const Range& r, Squares& q) {
     constexpr int E = 16 / sizeof(T);
+    const T* body = p + r.body;
     const int64_t vecs = (r.hi - r.body) / E;
-    float s = 0.f, big = 0.f;
-    auto add1 = [&](float x) {
-        s = fmaf(x, x, s);
-        big = fmaxf(big, fabsf(x));
-    };
-    if (r.lo + threadIdx.x < r.body) add1(Elem<T>::to_f(p[r.lo + threadIdx.x]));
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < vecs; i += kThreads) {
-        Pack<T, E> x;
-        x.load(p + r.body + i * E);
+    int64_t i = threadIdx.x;
+    for (; i + (kUnroll - 1) * kThreads < vecs; i += kUnroll * kThreads) {
+        Pack<T, E> x[kUnroll];
 #pragma unroll
-        for (int j = 0; j < E; ++j) add1(Elem<T>::to_f(x.e[j]));
+        for (int u = 0; u < kUnroll; ++u) x[u].load(body + (i + u * kThreads) * E);
+#pragma unroll
+        for (int u = 0; u < kUnroll; u += 32 / E) {
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = Elem<T>::to_f(x[u + j / E].e[j % E]);
+            q.add_all(f);
+        }
     }
-    const int64_t tail = r.body + vecs * E + threadIdx.x;
-    if (tail < r.hi) add1(Elem<T>::to_f(p[tail]));
-    // a NaN is in s whatever the largest of the others is
-    if (big == 0.f || (big >= 0x1p-50f && big <= 0x1p55f)) {
-        q.sum = add(q.sum, Pair{s, 0.f});
-        return;
+    for (; i < vecs; i += kThreads) {
+        Pack<T, E> x;
+        x.load(body + i * E);
+        float f[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) f[j] = Elem<T>::to_f(x.e[j]);
+        q.add_all(f);
     }
-    auto add64 = [&](T x) {
-        const double f = Elem<T>::to_f(x);
-        q.wide += f * f;
-    };
-    q.used_wide = true;
-    if (r.lo + threadIdx.x < r.body) add64(p[r.lo + threadIdx.x]);
-    for (int64_t i = threadIdx.x; i < vecs; i += kThreads)
-        for (int j = 0; j < E; ++j) add64(p[r.body + i * E + j]);
-    if (tail < r.hi) add64(p[tail]);
+    const int64_t head = r.lo + threadIdx.x, tail = r.body + vecs * E + threadIdx.x;
+    float f[2] = {0.f, 0.f};
+    if (head < r.body) f[0] = Elem<T>::to_f(p[head]);
+    if (tail < r.hi) f[1] = Elem<T>::to_f(p[tail]);
+    q.add_all(f);
 }
 
 __device__ __forceinline__ double warp_sum(double x) {
@@ -139,54 +176,71 @@ __device__ double block_sum(const Squares& q) {
     return s;
 }
 
-// Squares of the list's chunks `first`, `first + step`, ...
+// Chunks of block `b` of `blocks`.
 template <int N>
-__device__ __forceinline__ void list_squares(const GradList<N>& L, int64_t first, int64_t step,
+__device__ __forceinline__ int64_t share(const GradList<N>& L, int64_t b, int64_t blocks) {
+    return L.chunks / blocks * b + (L.chunks % blocks < b ? L.chunks % blocks : b);
+}
+
+template <int N>
+__device__ __forceinline__ void list_squares(const GradList<N>& L, int64_t b, int64_t blocks,
                                              Squares& q) {
-    for (int64_t c = first; c < L.chunks; c += step) {
-        const Range r = chunk_range(L, c);
-        const void* p = L.data[r.tensor];
-        switch (L.dtype[r.tensor]) {
+    each_part(L, share(L, b, blocks), share(L, b + 1, blocks), false, [&](int a, const Range& r) {
+        const void* p = L.data[a];
+        switch (L.dtype[a]) {
             case LL_F32: add_squares(static_cast<const float*>(p), r, q); break;
             case LL_F16: add_squares(static_cast<const __half*>(p), r, q); break;
             default: add_squares(static_cast<const __nv_bfloat16*>(p), r, q);
         }
-    }
+    });
 }
 
 template <typename T>
-__device__ void scale_range(T* __restrict__ p, const Range& r, float coef) {
+__device__ __forceinline__ void scale_range(T* __restrict__ p, const Range& r, float coef) {
     constexpr int E = 16 / sizeof(T);
+    T* body = p + r.body;
     const int64_t vecs = (r.hi - r.body) / E;
     auto one = [&](T x) { return Elem<T>::from_f(Elem<T>::to_f(x) * coef); };
-    if (r.lo + threadIdx.x < r.body) p[r.lo + threadIdx.x] = one(p[r.lo + threadIdx.x]);
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < vecs; i += kThreads) {
+    const int64_t head = r.lo + threadIdx.x, tail = r.body + vecs * E + threadIdx.x;
+    if (tail < r.hi) p[tail] = one(p[tail]);
+    // whole rounds from the end of the range back
+    constexpr int64_t kRound = kUnroll * kThreads;
+    const int64_t rest = vecs % kRound;
+    for (int64_t i = vecs - kRound; i >= rest; i -= kRound) {
+        Pack<T, E> x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) x[u].load(body + (i + u * kThreads + threadIdx.x) * E);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) x[u].e[j] = one(x[u].e[j]);
+            x[u].store(body + (i + u * kThreads + threadIdx.x) * E);
+        }
+    }
+    for (int64_t i = threadIdx.x; i < rest; i += kThreads) {
         Pack<T, E> x;
-        x.load(p + r.body + i * E);
+        x.load(body + i * E);
 #pragma unroll
         for (int j = 0; j < E; ++j) x.e[j] = one(x.e[j]);
-        x.store(p + r.body + i * E);
+        x.store(body + i * E);
     }
-    const int64_t tail = r.body + vecs * E + threadIdx.x;
-    if (tail < r.hi) p[tail] = one(p[tail]);
+    if (head < r.body) p[head] = one(p[head]);
 }
 
-// Chunks `last`, `last - step`, ... scaled for the norm.
+// Block b's chunks scaled for the norm, from the last back.
 template <int N>
-__device__ __forceinline__ void list_scale(const GradList<N>& L, int64_t last, int64_t step,
+__device__ __forceinline__ void list_scale(const GradList<N>& L, int64_t b, int64_t blocks,
                                            float norm, float max_norm) {
     const float c = max_norm / (norm + 1e-6f);
     if (c >= 1.f) return;  // a NaN goes on: it belongs in the gradients too
-    for (int64_t i = last; i >= 0; i -= step) {
-        const Range r = chunk_range(L, i);
-        void* p = const_cast<void*>(L.data[r.tensor]);
-        switch (L.dtype[r.tensor]) {
+    each_part(L, share(L, b, blocks), share(L, b + 1, blocks), true, [&](int a, const Range& r) {
+        void* p = const_cast<void*>(L.data[a]);
+        switch (L.dtype[a]) {
             case LL_F32: scale_range(static_cast<float*>(p), r, c); break;
             case LL_F16: scale_range(static_cast<__half*>(p), r, c); break;
             default: scale_range(static_cast<__nv_bfloat16*>(p), r, c);
         }
-    }
+    });
 }
 
 template <int N>
@@ -223,7 +277,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) grad_clip_kernel(
     const __grid_constant__ GradList<N> L, const float* __restrict__ norm, float max_norm) {
     wait_for_prerequisites();
-    list_scale(L, L.chunks - 1 - blockIdx.x, gridDim.x, __ldcg(norm), max_norm);
+    list_scale(L, blockIdx.x, gridDim.x, __ldcg(norm), max_norm);
 }
 
 // The norm of a short list, and with max_norm > 0 its clipping, by one cluster.
@@ -250,15 +304,13 @@ __global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kThreads)
     }
     __syncthreads();
     if (max_norm > 0.f)
-        list_scale(L, (L.chunks - 1 - blockIdx.x) / kSmallCtas * kSmallCtas + blockIdx.x, kSmallCtas,
-                   total, max_norm);
+        list_scale(L, blockIdx.x, kSmallCtas, total, max_norm);
     cluster_barrier();  // no CTA leaves while another reads its shared memory
 }
 
 // Fills L with the tensors of the list from `from` on; returns how many it took.
 template <int N>
-int64_t fill_list(const ll_tensor* t, int64_t count, int64_t from, int chunk, GradList<N>& L) {
-    L.chunk = chunk;
+int64_t fill_list(const ll_tensor* t, int64_t count, int64_t from, GradList<N>& L) {
     L.count = 0;
     L.chunks = 0;
     int64_t i = from;
@@ -270,9 +322,8 @@ int64_t fill_list(const ll_tensor* t, int64_t count, int64_t from, int chunk, Gr
         L.dtype[k] = static_cast<uint8_t>(t[i].dtype);
         L.first[k] = L.chunks;
         const int es = t[i].dtype == LL_F32 ? 4 : 2;
-        int64_t head = ((16 - (reinterpret_cast<uintptr_t>(t[i].data) & 15)) & 15) / es;
-        if (head > t[i].n) head = t[i].n;
-        const int64_t c = (t[i].n - head + chunk - 1) / chunk;
+        const int64_t size = kChunk / es, head = head_of(t[i].data, t[i].n, es);
+        const int64_t c = (t[i].n - head + size - 1) / size;
         L.chunks += c > 0 ? c : 1;
     }
     return i - from;
@@ -291,7 +342,7 @@ bool is_small(const ll_tensor* t, int64_t count) {
 cudaError_t launch_small(const ll_tensor* t, int64_t count, float max_norm, float* norm,
                          cudaStream_t s) {
     GradList<kFewTensors> L;
-    fill_list(t, count, 0, kSmallChunk, L);
+    fill_list(t, count, 0, L);
     note_launches(1);
     grad_small_kernel<<<kSmallCtas, kThreads, 0, s>>>(L, max_norm, norm);
     return cudaGetLastError();
@@ -301,7 +352,7 @@ template <int N, typename F>
 cudaError_t each_list(const ll_tensor* t, int64_t count, int num_sms, const F& launch) {
     GradList<N> L;
     for (int64_t i = 0; i < count;) {
-        i += fill_list(t, count, i, kChunk, L);
+        i += fill_list(t, count, i, L);
         if (L.count == 0) break;
         int64_t grid = int64_t(num_sms) * kBlocksPerSm;
         if (grid > kGradMaxBlocks) grid = kGradMaxBlocks;
