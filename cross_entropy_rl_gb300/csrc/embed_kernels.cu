@@ -76,6 +76,7 @@ bool rows16(const void* p, int64_t ld, size_t es) {
 
 #ifndef LL_GC
 #define LL_GC 3
+#define LL_SC 8
 #define LL_GR 4
 #endif
 // ----------------------------------------------------------------- gradient
@@ -90,7 +91,7 @@ bool rows16(const void* p, int64_t ld, size_t es) {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCtas = 8;         // CTAs of the sorting cluster for many tokens
+constexpr int kSortCtas = LL_SC;         // CTAs of the sorting cluster for many tokens
 constexpr int kDigitBits = 9;        // most bits of a sorting pass
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kStaged = 4096;        // keys a CTA holds in shared memory
@@ -103,11 +104,11 @@ constexpr int kFillRows = kSortWarps * kBins * 32;  // vocabulary rows of one bi
 #endif
 constexpr int kWindow = LL_W;          // sorted positions of a warp of the sums
 
-// Shared memory of the sort: counts, keys (two buffers where one CTA sorts
-// alone), places of the keys among their equals.
-constexpr int sort_smem_bytes(int ctas) {
-    return kSortWarps * kBins * 4 + kStaged * 8 * (ctas == 1 ? 2 : 1) + kStaged * 2;
-}
+// Shared memory of the sort: counts, keys, the digits' words (the second buffer
+// of the keys, empty as they are counted, where one CTA sorts alone), places of
+// the keys among their equals.
+constexpr int kSortSmem = kSortWarps * kBins * 8 + kStaged * 8 + kStaged * 2;
+static_assert(kStaged * 8 == kSortWarps * kBins * 4, "the words fill a buffer of keys");
 
 // Positions of a piece: few enough that a token of a third of a large batch is
 // spread over the device, and that at most 2048 pieces' partial sums are kept.
@@ -181,31 +182,15 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
     return s - x;
 }
 
-// m[r]: lanes whose digit d[r] (of `bits` bits, below 0: none) is this lane's.
-// One vote a bit, kRounds of them side by side: a vote and what hangs on it take
-// some 90 cycles, match.any 75 of the whole SM's where most lanes differ.
 constexpr int kRounds = 4;  // rounds of 32 keys of a warp at a time
-__device__ __forceinline__ void same_digits(const int (&d)[kRounds], int bits,
-                                            unsigned (&m)[kRounds]) {
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const unsigned any = __ballot_sync(0xffffffffu, d[r] >= 0);
-        m[r] = d[r] >= 0 ? any : 0;
-    }
-#pragma unroll 1
-    for (int b = 0; b < bits; ++b)
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            const unsigned set = __ballot_sync(0xffffffffu, d[r] >> b & 1);
-            m[r] &= d[r] >> b & 1 ? set : ~set;
-        }
-}
 
 // Least-significant-digit radix sort by one CTA or one cluster, stable, so that
 // the positions of a token stay ascending.  Each warp owns a run of the keys; a
-// pass counts the run's digits (one lane adds for all of its digit), scans the
-// counts over warps, CTAs and digits, and writes each key to its place.  Tokens
-// outside the table drop out in the first pass.  Runs of up to kWarpStaged keys
+// pass counts the run's digits, scans the counts over warps, CTAs and digits,
+// and writes each key to its place.  The lanes of equal digit find each other by
+// setting their bits in the digit's word of the warp (a vote for each bit of the
+// digit took 4x the time, match.any more), and one of them counts for all.
+// Tokens outside the table drop out in the first pass.  Runs of up to kWarpStaged keys
 // are staged in shared memory.  The loops are kept short: the sort is some ten
 // thousand cycles long and its instructions are fetched cold (eight rounds
 // unrolled, counting 300 tokens took 3.2k cycles instead of 0.9k).
@@ -215,7 +200,7 @@ __device__ void sort_tokens(const SortArgs& a) {
     constexpr Key kNone = ~0ull;
     int* hist = reinterpret_cast<int*>(sort_smem);  // [kSortWarps][bins]
     Key* keys = reinterpret_cast<Key*>(sort_smem + kSortWarps * kBins * 4);
-    uint16_t* places = reinterpret_cast<uint16_t*>(keys + kStaged * (CTAS == 1 ? 2 : 1));
+    uint16_t* places = reinterpret_cast<uint16_t*>(keys + kStaged * 2);
     __shared__ int total[kBins], base[kBins], scan[kSortWarps], grand;
     __shared__ int last_head[kSortWarps];
     static_assert(kBins == kSortThreads, "a thread per digit");
@@ -283,29 +268,38 @@ __device__ void sort_tokens(const SortArgs& a) {
         const int bins = 1 << db;
         set_run();
         if (staged && (CTAS > 1 || pass == 0)) stage();
-        for (int i = tid; i < kSortWarps * bins; i += kSortThreads) hist[i] = 0;
+        unsigned* words = reinterpret_cast<unsigned*>(CTAS == 1 ? dst : keys + kStaged);
+        for (int i = tid; i < kSortWarps * bins; i += kSortThreads) hist[i] = words[i] = 0;
         __syncthreads();
         int* count = hist + warp * bins;
+        unsigned* word = words + warp * bins;
+        // A lane's place among the keys of its digit so far; counts the digits.
+        auto place = [&](int d) {
+            if (d >= 0) atomicOr(word + d, 1u << lane);
+            __syncwarp();
+            const unsigned peers = d >= 0 ? word[d] : 0;
+            const int had = d >= 0 ? count[d] : 0;
+            __syncwarp();
+            if (d >= 0 && (peers & lt) == 0) {
+                count[d] = had + __popc(peers);
+                word[d] = 0;
+            }
+            __syncwarp();
+            return had + __popc(peers & lt);
+        };
         auto digit = [&](Key k) { return k == kNone ? -1 : static_cast<int>(k >> (32 + shift)) & (bins - 1); };
         const int place0 = static_cast<int>((mine - keys) % kStaged - beg);
 #pragma unroll 1
         for (int64_t i = beg + lane; i - lane < end; i += 32 * kRounds) {
             Key k[kRounds];
             int d[kRounds];
-            unsigned peers[kRounds];
             block(i, k);
 #pragma unroll
             for (int r = 0; r < kRounds; ++r) d[r] = digit(k[r]);
-            same_digits(d, db, peers);
 #pragma unroll
             for (int r = 0; r < kRounds; ++r) {
-                const int had = d[r] >= 0 ? count[d[r]] : 0;
-                __syncwarp();
-                if (d[r] >= 0) {
-                    if ((peers[r] & lt) == 0) count[d[r]] = had + __popc(peers[r]);
-                    if (staged) places[place0 + i + r * 32] = had + __popc(peers[r] & lt);
-                }
-                __syncwarp();
+                const int at = place(d[r]);
+                if (staged && d[r] >= 0) places[place0 + i + r * 32] = at;
             }
         }
         __syncthreads();
@@ -353,15 +347,10 @@ __device__ void sort_tokens(const SortArgs& a) {
                 for (int r = 0; r < kRounds; ++r)
                     at[r] = d[r] >= 0 ? count[d[r]] + base[d[r]] + places[place0 + i + r * 32] : 0;
             } else {
-                unsigned peers[kRounds];
-                same_digits(d, db, peers);
 #pragma unroll
                 for (int r = 0; r < kRounds; ++r) {
-                    const int had = d[r] >= 0 ? count[d[r]] : 0;
-                    __syncwarp();
-                    if (d[r] >= 0 && (peers[r] & lt) == 0) count[d[r]] = had + __popc(peers[r]);
-                    __syncwarp();
-                    at[r] = d[r] >= 0 ? had + base[d[r]] + __popc(peers[r] & lt) : 0;
+                    const int p = place(d[r]);
+                    at[r] = d[r] >= 0 ? p + base[d[r]] : 0;
                 }
             }
 #pragma unroll
@@ -794,10 +783,13 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, int 
     note_launches(1);
     const int ctas = e.N <= kStaged ? 1 : kSortCtas;
     auto* kernel = ctas == 1 ? embed_sort_kernel<1> : embed_sort_kernel<kSortCtas>;
-    const int smem = sort_smem_bytes(ctas);
-    const cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
     if (err != cudaSuccess) return err;
+    if (ctas > 8) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (err != cudaSuccess) return err;
+    }
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = ctas;
@@ -805,7 +797,7 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, int 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(accumulate ? ctas : kFillCtas);
     cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSortSmem;
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
