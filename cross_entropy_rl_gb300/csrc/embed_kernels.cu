@@ -98,7 +98,6 @@ constexpr int kFillBytes = 65536;    // of a block that fills rows beside the su
 constexpr int kFillRows = kSortWarps * kBins * 32;
 constexpr int64_t kShort = 8192;     // most tokens of the finer division below
 constexpr int kGradWarps = 8;
-constexpr int kGradCtas = 3;         // blocks an SM of the sums
 constexpr int kGradRows = 4;         // rows in flight of a warp of the sums
 
 // Shared memory of the sort: counts, keys, the digits' words (the second buffer
@@ -467,14 +466,34 @@ __device__ void sort_tokens(const SortArgs& a) {
     all_ctas();  // no CTA leaves while another reads its shared memory
 }
 
-// One row of a table set to +0 by thread `me` of `threads`.
-__device__ __forceinline__ void fill_row(char* p, int64_t bytes, int me, int threads) {
+// [p, p + bytes) set to +0 by thread `me` of `threads`.
+__device__ __forceinline__ void fill_zero(char* p, int64_t bytes, int me, int threads) {
     const int64_t vec = reinterpret_cast<uintptr_t>(p) % 16 == 0 ? bytes / 16 : 0;
 #pragma unroll 4
     for (int64_t i = me; i < vec; i += threads)
         reinterpret_cast<uint4*>(p)[i] = make_uint4(0, 0, 0, 0);
     for (int64_t i = vec * 16 + me * 2; i < bytes; i += 2 * threads)
         *reinterpret_cast<uint16_t*>(p + i) = 0;
+}
+
+// The first `rows` rows at p, but for those of the bits `used`; at once where all
+// are to be set and lie side by side.
+__device__ __forceinline__ void fill_rows_of(char* p, int64_t pitch, int64_t row_bytes, int rows,
+                                             unsigned used, int me, int threads) {
+    used &= rows < 32 ? (1u << rows) - 1 : ~0u;
+    if (used == 0 && pitch == row_bytes) {
+        fill_zero(p, rows * row_bytes, me, threads);
+        return;
+    }
+    for (int r = 0; r < rows; ++r)
+        if (!(used >> r & 1)) fill_zero(p + r * pitch, row_bytes, me, threads);
+}
+
+// Rows that are filled together, of about `bytes`: a power of two up to 32.
+__host__ __device__ inline int rows_together(int64_t row_bytes, int64_t bytes) {
+    int n = 32;
+    while (n > 1 && n * row_bytes > bytes) n /= 2;
+    return n;
 }
 
 // Rows of no token set to +0, by the clusters that do not sort: each takes a
@@ -511,10 +530,12 @@ __device__ void fill_rows(const SortArgs& a, int64_t cluster, int64_t clusters) 
             a.p.used[r0 / 32 + w] =
                 joined(w) | (done >= 32 ? ~0u : done > 0 ? (1u << done) - 1 : 0u);
         }
-        for (int64_t v = int64_t(rank) * kSortWarps + warp; v < now; v += ctas * kSortWarps) {
-            if (joined(v >> 5) >> (v & 31) & 1) continue;
-            fill_row(a.table + (r0 + v) * a.pitch, a.row_bytes, lane, 32);
-        }
+        const int step = rows_together(a.row_bytes, 8192);  // of a warp
+        for (int64_t v = (int64_t(rank) * kSortWarps + warp) * step; v < now;
+             v += ctas * kSortWarps * step)
+            fill_rows_of(a.table + (r0 + v) * a.pitch, a.pitch, a.row_bytes,
+                         static_cast<int>(now - v < step ? now - v : step),
+                         joined(v >> 5) >> (v & 31), lane, 32);
         __syncthreads();
         if (ctas > 1) cluster_barrier();  // the bitmaps may be overwritten
     }
@@ -537,7 +558,7 @@ struct GradArgs {
     SortPtrs p;
     // rows that are left to fill with +0 (accumulate = 0); fills = 0: none
     int64_t V, row_bytes;
-    int fill_rows;   // of a block: a power of two up to 32
+    int fill_rows;   // of a block
     unsigned fills;  // blocks that fill rows, spread among the others
 };
 
@@ -554,11 +575,12 @@ __device__ __forceinline__ TO grad_value(float s, float old) {
 // the table's row at each unit's end, are in flight together: one add per
 // element read is bound by HBM, and most units are one or two rows.  Measured at
 // 32768 tokens x 4096 bf16 added into 151936 FP32 rows, the whole call: 3 blocks
-// an SM of 4 rows 141 us, 4 of 4 (spilled) 162, 2 of 8 144; a warp per unit and
-// tile, its rows waited for unit by unit, 209; adding to the table in L2
+// an SM of 4 rows 141 us, 4 of 4 (spilled) 162, 2 of 8 144 (without the table's
+// rows in registers 4 of 4 spill nothing: 4096 x 2048 40 us, 3 of 4 44); a warp
+// per unit and tile, its rows waited for unit by unit, 209; adding to the table in L2
 // (red.v4.f32) instead of reading it 164.
 template <typename TI, typename TO, int E, int C, int R, bool ADD>
-__global__ void __launch_bounds__(32 * kGradWarps, kGradCtas) embed_grad_kernel(
+__global__ void __launch_bounds__(32 * kGradWarps, ADD ? 3 : 4) embed_grad_kernel(
     const TI* __restrict__ g, TO* __restrict__ dW, const __grid_constant__ GradArgs a) {
     const int lane = threadIdx.x & 31;
     wait_for_prerequisites();
@@ -571,11 +593,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradCtas) embed_grad_kernel(
         block = block < 2 * turns ? block >> 1 : block - turns;
         if (fill) {
             const int64_t v0 = block * a.fill_rows;
-            const unsigned used = a.p.used[v0 / 32] >> (v0 % 32);
-            for (int r = 0; r < a.fill_rows && v0 + r < a.V; ++r)
-                if (!(used >> r & 1))
-                    fill_row(reinterpret_cast<char*>(dW + (v0 + r) * a.ldw), a.row_bytes,
-                             threadIdx.x, 32 * kGradWarps);
+            fill_rows_of(reinterpret_cast<char*>(dW + v0 * a.ldw), a.ldw * int64_t(sizeof(TO)),
+                         a.row_bytes, static_cast<int>(a.V - v0 < a.fill_rows ? a.V - v0 : a.fill_rows),
+                         a.p.used[v0 / 32] >> (v0 % 32), threadIdx.x, 32 * kGradWarps);
             return;
         }
     }
@@ -737,8 +757,7 @@ cudaError_t grad_typed(const EmbedArgs& e, bool vec, int accumulate, GradArgs a,
     const int64_t sums_blocks = (items + kGradWarps - 1) / kGradWarps;
     a.V = e.V;
     a.row_bytes = e.D * int64_t(sizeof(TO));
-    a.fill_rows = 32;
-    while (a.fill_rows > 1 && a.fill_rows * a.row_bytes > kFillBytes) a.fill_rows /= 2;
+    a.fill_rows = rows_together(a.row_bytes, kFillBytes);
     a.fills = accumulate ? 0 : static_cast<unsigned>((e.V + a.fill_rows - 1) / a.fill_rows);
     const int64_t blocks = sums_blocks + a.fills;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
