@@ -9,13 +9,14 @@ namespace {
 
 // ------------------------------------------------------------------- lookup
 // One multiply per element: bound by HBM (a row read, a row written).  A warp
-// takes one row's tile of kLookupTile chunks of E elements; all its loads are
-// issued before the first store.
-constexpr int kLookupUnroll = 4;
-constexpr int kLookupTile = 32 * kLookupUnroll;
+// takes one row's tile of 32 U chunks of E elements; all its loads are issued
+// before the first store.  32768 x 4096 bf16 of 151936 rows: 59 us, 0.92 of the
+// copy bandwidth (U = 8: 61.5 us).  Rows that do not start on 16-byte boundaries
+// go element by element, U = 16 of them in flight a lane: 10007 x 1001 FP32 to
+// FP16 8.7 us (U = 4: 12.6, 8: 9.3).
 constexpr int kLookupWarps = 8;
 
-template <typename TI, typename TO, int E>
+template <typename TI, typename TO, int E, int U>
 __global__ void __launch_bounds__(32 * kLookupWarps) embed_fwd_kernel(
     const TI* __restrict__ W, int64_t ldw, const int64_t* __restrict__ tokens, int64_t N,
     int64_t D, int64_t V, int64_t v0, float scale, TO* __restrict__ out, int64_t ldo) {
@@ -27,16 +28,16 @@ __global__ void __launch_bounds__(32 * kLookupWarps) embed_fwd_kernel(
     const TI* src = W + (in ? v : 0) * ldw;
     TO* dst = out + n * ldo;
     const int64_t chunks = (D + E - 1) / E;
-    for (int64_t c0 = int64_t(blockIdx.y) * kLookupTile + lane; c0 < chunks;
-         c0 += int64_t(gridDim.y) * kLookupTile) {
-        Pack<TI, E> x[kLookupUnroll];
+    for (int64_t c0 = int64_t(blockIdx.y) * (32 * U) + lane; c0 < chunks;
+         c0 += int64_t(gridDim.y) * (32 * U)) {
+        Pack<TI, E> x[U];
 #pragma unroll
-        for (int u = 0; u < kLookupUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int64_t c = (c0 + 32 * u) * E;
             if (in && c + E <= D) x[u].load(src + c);
         }
 #pragma unroll
-        for (int u = 0; u < kLookupUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int64_t c = (c0 + 32 * u) * E;
             if (c + E <= D) {
                 Pack<TO, E> y;
@@ -56,16 +57,18 @@ template <typename TI, typename TO>
 cudaError_t fwd_typed(const EmbedArgs& a, bool vec, cudaStream_t s) {
     constexpr int E = 16 / (sizeof(TI) < sizeof(TO) ? sizeof(TI) : sizeof(TO));
     const int64_t chunks = vec ? (a.D + E - 1) / E : a.D;
-    const int64_t tiles = (chunks + kLookupTile - 1) / kLookupTile;
+    constexpr int U = 4, U1 = 16;
+    const int tile = 32 * (vec ? U : U1);
+    const int64_t tiles = (chunks + tile - 1) / tile;
     const dim3 grid(static_cast<unsigned>((a.N + kLookupWarps - 1) / kLookupWarps),
                     static_cast<unsigned>(tiles < 65535 ? tiles : 65535));
     const TI* W = static_cast<const TI*>(a.rows);
     TO* out = static_cast<TO*>(a.table);
     if (vec)
-        embed_fwd_kernel<TI, TO, E><<<grid, 32 * kLookupWarps, 0, s>>>(
+        embed_fwd_kernel<TI, TO, E, U><<<grid, 32 * kLookupWarps, 0, s>>>(
             W, a.ld_rows, a.tokens, a.N, a.D, a.V, a.v0, a.scale, out, a.ld_table);
     else
-        embed_fwd_kernel<TI, TO, 1><<<grid, 32 * kLookupWarps, 0, s>>>(
+        embed_fwd_kernel<TI, TO, 1, U1><<<grid, 32 * kLookupWarps, 0, s>>>(
             W, a.ld_rows, a.tokens, a.N, a.D, a.V, a.v0, a.scale, out, a.ld_table);
     return cudaGetLastError();
 }
