@@ -100,6 +100,7 @@ constexpr int kFillBytes = 65536;    // of a block that fills rows beside the su
 // vocabulary rows of one bitmap, which takes the place of the counts
 constexpr int kFillRows = kSortWarps * kBins * 32;
 constexpr int64_t kShort = 8192;     // most tokens of the finer division below
+constexpr int kFewPieces = 8;        // pieces of a token that one warp adds up
 constexpr int kGradWarps = 8;
 constexpr int kGradRows = 4;         // rows in flight of a warp of the sums
 
@@ -135,8 +136,8 @@ struct Long {
 };
 
 struct SortHead {
-    int valid;  // tokens of the table: entries
-    int longs;
+    int valid;         // tokens of the table: entries
+    int longs, huges;  // tokens of 2 .. kFewPieces units, of more
 };
 
 struct SortPtrs {
@@ -145,7 +146,8 @@ struct SortPtrs {
     Entry* entries;                   // [N]
     int* windows;                     // [ceil(N / window) + 1] start of the unit of each
                                       // window-th entry
-    Long* longs;                      // [ceil(N / K)], in any order
+    Long* longs;                      // [ceil(N / K)], in any order: the longs from the
+                                      // front on, the huges from the back
     unsigned* used;                   // [ceil(V / 32)] rows that are not to be filled any more
     float* part;                      // [2 ceil(N / K), Dp] sums of pieces
     int64_t Dp;
@@ -155,7 +157,7 @@ struct SortArgs {
     const int64_t* tokens;
     int64_t N, V, v0;
     int bits, passes;  // of a row index; sorting passes
-    int K, window;
+    int K, window, slots;
     SortPtrs p;
     // rows of no token are set to +0 (accumulate = 0), else null
     char* table;
@@ -218,7 +220,8 @@ __device__ void sort_tokens(const SortArgs& a) {
         if (CTAS > 1) cluster_barrier();
     };
 
-    if (rank == 0 && tid == 0) a.p.head->longs = 0;  // ahead of barriers of all CTAs
+    // ahead of barriers of all CTAs
+    if (rank == 0 && tid == 0) a.p.head->longs = a.p.head->huges = 0;
 
     int64_t M = a.N, beg, end;
     bool staged;
@@ -455,9 +458,12 @@ __device__ void sort_tokens(const SortArgs& a) {
                 a.p.entries[i] = Entry{static_cast<unsigned>(k[r]) | (unit_ends ? kTop : 0u),
                                        row | (more ? kTop : 0u)};
                 if (i % a.window == 0) a.p.windows[i / a.window] = i - in;
-                if (token_ends && i - h >= a.K)
-                    a.p.longs[atomicAdd(&a.p.head->longs, 1)] =
+                if (token_ends && i - h >= a.K) {
+                    const bool huge = i - h >= a.K * kFewPieces;
+                    const int at = atomicAdd(huge ? &a.p.head->huges : &a.p.head->longs, 1);
+                    a.p.longs[huge ? a.slots - 1 - at : at] =
                         Long{h, i + 1 - h, static_cast<int>(row), 0};
+                }
             }
             if (heads[r]) head = b + 31 - __clz(heads[r]);
         }
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(kSortThreads, 2)
 struct GradArgs {
     int64_t ldg, D, ldw;
     float scale;
-    int tiles, K, window;
+    int tiles, K, window, slots;
     SortPtrs p;
     // rows that are left to fill with +0 (accumulate = 0); fills = 0: none
     int64_t V, row_bytes;
@@ -691,53 +697,72 @@ __global__ void __launch_bounds__(32 * kGradWarps, ADD ? 3 : 4) embed_grad_kerne
     }
 }
 
-// Tokens of several pieces: a block takes 32 packs of columns of one, each warp
-// an equal run of its pieces, and the warps' sums are added in order.
+// The scaled sum s of E columns stored to (or on top of) a row.
+template <typename TO, int E, bool ADD>
+__device__ __forceinline__ void put_row(TO* p, float scale, const float (&s)[E]) {
+    Pack<TO, E> y;
+    if (ADD) y.load(p);
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        y.e[j] = grad_value<TO>(scale * s[j], ADD ? Elem<TO>::to_f(y.e[j]) : 0.f);
+    y.store(p);
+}
+
+// Tokens of several pieces.  Of up to kFewPieces: a warp takes 32 packs of
+// columns and adds the pieces in order.  Of more: a block takes kLanes packs;
+// its 256 / kLanes groups of lanes each add every so-manieth piece, and the
+// groups' sums are added in order.  The order depends on the number of pieces.
 template <typename TO, int E, bool ADD>
 __global__ void __launch_bounds__(32 * kGradWarps) embed_join_kernel(
     TO* __restrict__ dW, const __grid_constant__ GradArgs a) {
-    __shared__ float sums[kGradWarps][32 * E];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kLanes = 8, kGroups = 32 * kGradWarps / kLanes;
+    __shared__ float sums[kGroups][kLanes * E];
     wait_for_prerequisites();
-    const int64_t tiles = (a.D + 32 * E - 1) / (32 * E);
-    const int64_t items = a.p.head->longs * tiles;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const Long l = a.p.longs[it / tiles];
-        const int64_t c = (it % tiles * 32 + lane) * E;
-        const int n = (l.count + a.K - 1) / a.K;
-        const int per = (n + kGradWarps - 1) / kGradWarps;
-        const int p0 = warp * per, p1 = p0 + per < n ? p0 + per : n;
-        const bool odd = l.count % a.K != 0;
-        float s[E];
+    const int lane = threadIdx.x & 31;
+    auto pieces = [&](const Long& l) { return (l.count + a.K - 1) / a.K; };
+    // sum of the pieces i, i + step, ... of the columns from c on
+    auto add_up = [&](const Long& l, int64_t c, int i, int step, float (&s)[E]) {
+        const int n = pieces(l);
+        const int odd = l.count % a.K != 0 ? n - 1 : n;  // the short last piece
+        const float* src = a.p.part + int64_t(l.start / a.K) * 2 * a.p.Dp + c;
 #pragma unroll
         for (int j = 0; j < E; ++j) s[j] = 0.f;
-        if (c < a.D) {
-            const float* src = a.p.part + int64_t(l.start / a.K) * 2 * a.p.Dp + c;
 #pragma unroll 8
-            for (int i = p0; i < p1; ++i) {
-                Pack<float, E> x;
-                x.load(src + (i * int64_t(2) + (odd && i == n - 1)) * a.p.Dp);
+        for (; i < n; i += step) {
+            Pack<float, E> x;
+            x.load(src + (i * int64_t(2) + (i == odd)) * a.p.Dp);
 #pragma unroll
-                for (int j = 0; j < E; ++j) s[j] += x.e[j];
-            }
+            for (int j = 0; j < E; ++j) s[j] += x.e[j];
         }
+    };
+    const SortHead head = *a.p.head;
+    const int64_t narrow = (a.D + kLanes * E - 1) / (kLanes * E);
+    for (int64_t it = blockIdx.x; it < head.huges * narrow; it += gridDim.x) {
+        const Long l = a.p.longs[a.slots - 1 - it / narrow];
+        const int group = threadIdx.x / kLanes, at = threadIdx.x % kLanes;
+        const int64_t c = (it % narrow * kLanes + at) * E;
+        float s[E] = {};
+        if (c < a.D) add_up(l, c, group, kGroups, s);
 #pragma unroll
-        for (int j = 0; j < E; ++j) sums[warp][j * 32 + lane] = s[j];
+        for (int j = 0; j < E; ++j) sums[group][j * kLanes + at] = s[j];
         __syncthreads();
-        if (warp == 0 && c < a.D) {
-            const int used = (n + per - 1) / per;
-            TO* row = dW + int64_t(l.row) * a.ldw + c;
-            Pack<TO, E> y;
-            if (ADD) y.load(row);
+        if (group == 0 && c < a.D) {
+            for (int g = 1; g < kGroups; ++g)
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                float f = s[j];
-                for (int w = 1; w < used; ++w) f += sums[w][j * 32 + lane];
-                y.e[j] = grad_value<TO>(a.scale * f, ADD ? Elem<TO>::to_f(y.e[j]) : 0.f);
-            }
-            y.store(row);
+                for (int j = 0; j < E; ++j) s[j] += sums[g][j * kLanes + at];
+            put_row<TO, E, ADD>(dW + int64_t(l.row) * a.ldw + c, a.scale, s);
         }
         __syncthreads();
+    }
+    const int64_t wide = (a.D + 32 * E - 1) / (32 * E);
+    for (int64_t it = blockIdx.x * int64_t(kGradWarps) + (threadIdx.x >> 5); it < head.longs * wide;
+         it += int64_t(gridDim.x) * kGradWarps) {
+        const Long l = a.p.longs[it / wide];
+        const int64_t c = (it % wide * 32 + lane) * E;
+        if (c >= a.D) continue;
+        float s[E];
+        add_up(l, c, 0, 1, s);
+        put_row<TO, E, ADD>(dW + int64_t(l.row) * a.ldw + c, a.scale, s);
     }
 }
 
@@ -852,6 +877,7 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, int 
     a.passes = (a.bits + kDigitBits - 1) / kDigitBits;
     a.K = static_cast<int>(piece_rows(e.N));
     a.window = window_rows(e.N);
+    a.slots = static_cast<int>((e.N + a.K - 1) / a.K);
     a.p = grad_layout(e.N, e.D, e.V, ws, &bytes);
     const int64_t es = e.table_dtype == LL_F32 ? 4 : 2;
     a.table = accumulate ? nullptr : static_cast<char*>(e.table);
@@ -898,6 +924,7 @@ cudaError_t launch_embed_bwd(const EmbedArgs& e, int accumulate, void* ws, int n
     a.tiles = 0;
     a.K = static_cast<int>(piece_rows(e.N));
     a.window = window_rows(e.N);
+    a.slots = static_cast<int>((e.N + a.K - 1) / a.K);
     a.p = grad_layout(e.N, e.D, e.V, ws, &bytes);
     switch (e.dtype * 3 + e.table_dtype) {
         case LL_F32 * 3 + LL_F32: return grad_typed<float, float>(e, vec, accumulate, a, num_sms, s);
