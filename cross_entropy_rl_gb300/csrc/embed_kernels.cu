@@ -173,6 +173,16 @@ __device__ __forceinline__ int ld_cluster(const int* local, uint32_t rank) {
     return v;
 }
 
+__device__ __forceinline__ unsigned long long ld_cluster64(const void* local, uint32_t rank) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr(local, rank)));
+    return v;
+}
+__device__ __forceinline__ void st_cluster64(void* local, uint32_t rank, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(local, rank)), "l"(v)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_ctas() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
@@ -196,10 +206,12 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
 // and writes each key to its place.  The lanes of equal digit find each other by
 // setting their bits in the digit's word of the warp (a vote for each bit of the
 // digit took 4x the time, match.any more), and one of them counts for all.
-// Tokens outside the table drop out in the first pass.  Runs of up to kWarpStaged keys
-// are staged in shared memory.  The loops are kept short: the sort is some ten
-// thousand cycles long and its instructions are fetched cold (eight rounds
-// unrolled, counting 300 tokens took 3.2k cycles instead of 0.9k).
+// Tokens outside the table drop out in the first pass.  Up to kStaged keys a CTA
+// stay in shared memory: a CTA's runs lie side by side there, and a key goes to
+// its place in the other buffer of the CTA whose run that is.  The loops are kept
+// short: the sort is some ten thousand cycles long and its instructions are
+// fetched cold (eight rounds unrolled, counting 300 tokens took 3.2k cycles
+// instead of 0.9k).  300 / 4096 / 32768 tokens: 6 / 12 / 21 us.
 template <int CTAS>
 __device__ void sort_tokens(const SortArgs& a) {
     typedef unsigned long long Key;
@@ -224,19 +236,21 @@ __device__ void sort_tokens(const SortArgs& a) {
     if (rank == 0 && tid == 0) a.p.head->longs = a.p.head->huges = 0;
 
     int64_t M = a.N, beg, end;
-    bool staged;
-    Key* mine;  // the warp's staged keys
+    const bool staged = CTAS == 1 || M <= CTAS * kStaged;
+    unsigned run;   // keys of a warp
+    Key* mine;      // the warp's staged keys
     auto set_run = [&]() {
         const int64_t per = ((M + 31) / 32 + kWarps - 1) / kWarps * 32;
         beg = me * per < M ? me * per : M;
         end = beg + per < M ? beg + per : M;
-        staged = per <= kWarpStaged;  // always, where one CTA sorts alone
-        mine = keys + (CTAS == 1 ? beg : int64_t(warp) * kWarpStaged);
+        run = static_cast<unsigned>(per);
+        mine = keys + warp * per;
     };
     // Sorted keys of the passes, alternately in two buffers; ahead of the first,
     // keys made of the tokens.
     const Key* src = nullptr;
-    Key* dst = CTAS == 1 ? keys + kStaged : a.p.buf0;
+    Key* dst = a.p.buf0;
+    Key* other = keys + kStaged;  // staged keys of the next pass
     auto key_of = [&](int64_t i, int64_t y) -> Key {
         const int64_t v = y - a.v0;
         if (y < a.v0 || v >= a.V) return kNone;
@@ -247,17 +261,16 @@ __device__ void sort_tokens(const SortArgs& a) {
     };
     auto stage = [&]() {
         if (beg >= end) return;
-        int64_t x[kWarpStaged / 32];
-        const int64_t* from = src ? reinterpret_cast<const int64_t*>(src) : a.tokens;
+        int64_t y[kWarpStaged / 32];
 #pragma unroll
         for (int q = 0; q < kWarpStaged / 32; ++q) {
             const int64_t i = beg + q * 32 + lane;
-            x[q] = __ldcg(from + (i < end ? i : end - 1));
+            y[q] = __ldcg(a.tokens + (i < end ? i : end - 1));
         }
 #pragma unroll
         for (int q = 0; q < kWarpStaged / 32; ++q) {
             const int64_t i = beg + q * 32 + lane;
-            if (i < end) mine[q * 32 + lane] = src ? static_cast<Key>(x[q]) : key_of(i, x[q]);
+            if (i < end) mine[q * 32 + lane] = key_of(i, y[q]);
         }
     };
     // Keys of kRounds rounds from i on, i the lane's first.
@@ -274,8 +287,8 @@ __device__ void sort_tokens(const SortArgs& a) {
         const int db = (a.bits - shift + (a.passes - pass) - 1) / (a.passes - pass);
         const int bins = 1 << db;
         set_run();
-        if (staged && (CTAS > 1 || pass == 0)) stage();
-        unsigned* words = reinterpret_cast<unsigned*>(CTAS == 1 ? dst : keys + kStaged);
+        if (staged && pass == 0) stage();
+        unsigned* words = reinterpret_cast<unsigned*>(other);
         for (int i = tid; i < kSortWarps * bins; i += kSortThreads) hist[i] = words[i] = 0;
         __syncthreads();
         int* count = hist + warp * bins;
@@ -344,6 +357,8 @@ __device__ void sort_tokens(const SortArgs& a) {
         if (tid < bins) base[tid] = under + low + before;
         if (tid == 0) grand = sum;
         __syncthreads();
+        if (pass == 0) M = grand;
+        const unsigned share = ((M + 31) / 32 + kWarps - 1) / kWarps * 32 * kSortWarps;  // of a CTA
 #pragma unroll 1
         for (int64_t i = beg + lane; i - lane < end; i += 32 * kRounds) {
             Key k[kRounds];
@@ -363,15 +378,23 @@ __device__ void sort_tokens(const SortArgs& a) {
                 }
             }
 #pragma unroll
-            for (int r = 0; r < kRounds; ++r)
-                if (d[r] >= 0) dst[at[r]] = k[r];
+            for (int r = 0; r < kRounds; ++r) {
+                if (d[r] < 0) continue;
+                if (!staged) {
+                    dst[at[r]] = k[r];
+                } else if (CTAS == 1) {
+                    other[at[r]] = k[r];
+                } else {
+                    const unsigned to = static_cast<unsigned>(at[r]) / share;
+                    st_cluster64(other + (at[r] - to * share), to, k[r]);
+                }
+            }
         }
         shift += db;
-        if (pass == 0) M = grand;
-        if (CTAS == 1) {
+        if (staged) {
             Key* t = keys;
-            keys = dst;
-            dst = t;
+            keys = other;
+            other = t;
         } else {
             src = dst;
             dst = dst == a.p.buf0 ? a.p.buf1 : a.p.buf0;
@@ -382,11 +405,18 @@ __device__ void sort_tokens(const SortArgs& a) {
     // The entries with their units' ends.  All that a warp needs from the runs
     // ahead of its own is where the last token started.
     set_run();
-    if (CTAS > 1 && staged) stage();
-    __syncwarp();
+    const unsigned share = run * kSortWarps;
     auto row_at = [&](int64_t i) -> unsigned {
         if (i < 0 || i >= M) return ~0u;
-        const Key k = CTAS == 1 ? keys[i] : __ldcg(src + i);
+        Key k;
+        if (!staged) {
+            k = __ldcg(src + i);
+        } else if (CTAS == 1) {
+            k = keys[i];
+        } else {
+            const unsigned at = static_cast<unsigned>(i) / share;
+            k = ld_cluster64(keys + (i - int64_t(at) * share), at);
+        }
         return static_cast<unsigned>(k >> 32);
     };
     const unsigned row_before = row_at(beg - 1), row_after = row_at(end);
@@ -891,13 +921,9 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, int 
     note_launches(1);
     const int ctas = e.N <= kStaged ? 1 : kSortCtas;
     auto* kernel = ctas == 1 ? embed_sort_kernel<1> : embed_sort_kernel<kSortCtas>;
-    cudaError_t err =
+    const cudaError_t err =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
     if (err != cudaSuccess) return err;
-    if (ctas > 8) {
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (err != cudaSuccess) return err;
-    }
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = ctas;

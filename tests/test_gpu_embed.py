@@ -244,3 +244,31 @@ def test_streams_and_graphs(lib):
     assert bits_equal(out, lib.embed_forward(W, y))
     assert bits_equal(dW, lib.embed_backward(g, y, V))
     assert lib.check_status() == 0
+
+
+@pytest.mark.parametrize("N", [255, 257, 4095, 4096, 4097, 32767, 32768, 32769, 70001])
+@pytest.mark.parametrize("V,invalid", [(1, 0.0), (2, 0.97), (513, 0.0), (511, 0.97), (300000, 0.05),
+                                       (140000000, 0.97)])
+def test_gradient_where_the_sort_changes(lib, N, V, invalid):
+    """Around the sizes at which the sort goes from one block to a cluster and out
+    of shared memory, with most tokens dropped, for one to four passes over the digits.
+    Small whole numbers, whose sums are exact in any order."""
+    D = 8 if V < 1000000 else 1
+    rng = np.random.default_rng(N + V)
+    y = ids(N, V, N, hot=0.1, invalid=invalid)
+    near = rng.random(N) < 0.3  # tokens side by side in the table too
+    y = np.where(near & (y >= 0) & (y < V), np.minimum(y % 300, V - 1), y)
+    g = torch.from_numpy(rng.integers(-3, 4, (N, D))).to(torch.bfloat16).cuda()
+    ok = (y >= 0) & (y < V)
+    rows, back = np.unique(y[ok], return_inverse=True)
+    want = np.zeros((len(rows), D))
+    np.add.at(want, back, host64(g)[ok])
+    at = torch.from_numpy(rows).cuda()
+    got = lib.embed_backward(g, torch.from_numpy(y).cuda(), V, scale=2.0)
+    assert (host64(got[at]) == 2 * want).all()
+    got[at] = 0
+    assert float(got.abs().max()) == 0
+    lib.embed_backward(g, torch.from_numpy(y).cuda(), V, accumulate=True, out=got.fill_(1))
+    assert (host64(got[at]) == 1 + want).all()
+    got[at] = 1
+    assert float(got.min()) == 1 == float(got.max())
