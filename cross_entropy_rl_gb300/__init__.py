@@ -803,24 +803,29 @@ class Tensor(ctypes.Structure):
 def _tensor_list(tensors):
     """(ll_tensor records as three 64-bit integers each, device) of gradients
     that each fill their memory without gaps, in any order of their dimensions."""
-    torch = _torch()
+    T = _torch().Tensor
     codes = _codes()
-    words = []
-    dev = where = None
-    for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"tensor {i} must be a torch.Tensor")
-        code = codes.get(t.dtype)
-        if code is None:
-            raise TypeError(f"tensor {i}: unsupported dtype {t.dtype}")
-        if dev is None:
-            dev, where = t.device, t.get_device()
-        elif t.get_device() != where:
-            raise ValueError(f"tensor {i}: on {t.device}, expected {dev}")
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"tensor {i}: its elements must fill their memory without gaps")
-        words += (t.data_ptr(), t.numel(), code)  # dtype and reserved = 0 share a word
-    return array.array("q", words), dev
+    if not isinstance(tensors, (list, tuple)):
+        tensors = list(tensors)
+    words = array.array("q", bytes(24 * len(tensors)))  # the dtype shares its word with reserved = 0
+    try:
+        words[0::3] = array.array("q", map(T.data_ptr, tensors))
+        words[1::3] = array.array("q", map(T.numel, tensors))
+        words[2::3] = array.array("q", [codes[t.dtype] for t in tensors])
+        alike = len(set(map(T.get_device, tensors))) <= 1 and all(map(T.is_contiguous, tensors))
+    except (TypeError, KeyError):
+        alike = False
+    if not alike:
+        for i, t in enumerate(tensors):
+            if not isinstance(t, T):
+                raise TypeError(f"tensor {i} must be a torch.Tensor")
+            if t.dtype not in codes:
+                raise TypeError(f"tensor {i}: unsupported dtype {t.dtype}")
+            if t.device != tensors[0].device:
+                raise ValueError(f"tensor {i}: on {t.device}, expected {tensors[0].device}")
+            if not t.is_contiguous() and not _dense(t):
+                raise ValueError(f"tensor {i}: its elements must fill their memory without gaps")
+    return words, tensors[0].device if tensors else None
 
 
 def _dense(t):

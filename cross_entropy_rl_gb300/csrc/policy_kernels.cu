@@ -83,11 +83,18 @@ struct SeqWalk {
     }
 };
 
-// exp(d) - d - 1.  For small |d| the exponential's rounding alone (6e-8) would
-// be more than the result (d^2 / 2), so there it is d^2 times the Taylor
-// polynomial of (e^d - 1 - d) / d^2 up to d^9 (below 2^-34 of it left out).
-__device__ __forceinline__ float exp_rest2(float d) {
-    if (fabsf(d) >= 0.5f) return expf(d) - d - 1.f;
+// exp(d) - d - 1 and exp(d) - 1.  For small |d| the exponential's rounding alone
+// (6e-8) would be more than the first (d^2 / 2), so there it is d^2 times the
+// Taylor polynomial of (e^d - 1 - d) / d^2 up to d^9 (below 2^-27 of it left out),
+// and the second is that and d.
+struct Exp {
+    float rest2, rest1;
+};
+__device__ __forceinline__ Exp exp_rests(float d) {
+    if (fabsf(d) >= 1.f) {
+        const float e = expf(d);
+        return {e - d - 1.f, e - 1.f};
+    }
     float q = 1.f / 39916800.f;
     q = fmaf(q, d, 1.f / 3628800.f);
     q = fmaf(q, d, 1.f / 362880.f);
@@ -98,7 +105,8 @@ __device__ __forceinline__ float exp_rest2(float d) {
     q = fmaf(q, d, 1.f / 24.f);
     q = fmaf(q, d, 1.f / 6.f);
     q = fmaf(q, d, 0.5f);
-    return d * d * q;
+    q = d * d * q;
+    return {q, d + q};
 }
 
 // delta against a border held in 64 bits.  The FP32 difference is within 2^-24
@@ -132,9 +140,9 @@ __device__ __forceinline__ Token token_loss(const PolicyArgs& a, float logp, flo
     t.grad = t.clipped ? 0.f : pg;
     t.k = 0.f;
     if (a.ref) {
-        const float d = ref - logp;
-        t.k = exp_rest2(d);
-        if (a.beta != 0.f) t.grad -= a.beta * expm1f(d);
+        const Exp e = exp_rests(ref - logp);
+        t.k = e.rest2;
+        if (a.beta != 0.f) t.grad -= a.beta * e.rest1;
     }
     return t;
 }
@@ -175,9 +183,12 @@ __device__ __forceinline__ void count_sequences(const PolicyArgs& a, const Group
             atomicAdd(&ws->full, 1ull);
         count = 0;
     };
+    bool ahead = unmasked(a, g.beg * 32 + lane), ahead2 = unmasked(a, g.beg * 32 + 32 + lane);
 #pragma unroll 1
     for (int64_t i = g.beg; i < g.end; ++i) {
-        const bool in = unmasked(a, i * 32 + lane);
+        const bool in = ahead;  // the masks of two groups are on their way
+        ahead = ahead2;
+        ahead2 = unmasked(a, i * 32 + 64 + lane);
         const int b = walk.at(a, i * 32, lane);
         if (walk.uniform) {
             const unsigned m = __ballot_sync(0xffffffffu, in && b >= 0);
