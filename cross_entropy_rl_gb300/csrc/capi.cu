@@ -1310,11 +1310,11 @@ int ll_embed_backward(const void* grad_out, int64_t ldg, int dtype, const int64_
     const EmbedArgs a{grad_out, ldg, dtype, tokens, N, D, V, v0, scale, grad_weight, ldw, dw_dtype};
     {
         Phase ph("embed_sort", s);
-        const cudaError_t e = launch_embed_sort(a, accumulate, workspace, dev.num_sms, s);
+        const cudaError_t e = launch_embed_sort(a, accumulate, workspace, dev, s);
         if (e != cudaSuccess) return cuda_status(e);
     }
     Phase ph("embed_grad", s);
-    return cuda_status(launch_embed_bwd(a, accumulate, workspace, dev.num_sms, s));
+    return cuda_status(launch_embed_bwd(a, accumulate, workspace, dev, s));
 }
 
 size_t ll_policy_workspace_size(int64_t N, int64_t n_seqs) {

@@ -2,6 +2,8 @@
 //
 //   forward   out[n, :] = scale * W[y_n - v0, :]  (+0 rows for other tokens)
 //   backward  dW[v, :] (+)= scale * sum_{n: y_n - v0 = v} g[n, :]
+#include <atomic>
+
 #include "ll_device.cuh"
 
 namespace ll {
@@ -875,7 +877,8 @@ static SortPtrs grad_layout(int64_t N, int64_t D, int64_t V, void* ws, size_t* b
     q.buf0 = reinterpret_cast<unsigned long long*>(take(size_t(N) * 8));
     q.buf1 = reinterpret_cast<unsigned long long*>(take(size_t(N) * 8));
     q.entries = reinterpret_cast<Entry*>(take(size_t(N) * sizeof(Entry)));
-    q.windows = reinterpret_cast<int*>(take(size_t((N + window_rows(N) - 1) / window_rows(N) + 1) * 4));
+    const int64_t w = window_rows(N);
+    q.windows = reinterpret_cast<int*>(take(size_t((N + w - 1) / w + 1) * 4));
     q.longs = reinterpret_cast<Long*>(take(size_t(slots) * sizeof(Long)));
     q.used = reinterpret_cast<unsigned*>(take(size_t((V + 31) / 32) * 4));
     q.part = reinterpret_cast<float*>(take(size_t(2 * slots) * size_t(q.Dp) * 4));
@@ -895,7 +898,7 @@ static int bits_of(int64_t V) {
     return b;
 }
 
-cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, int num_sms,
+cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, const DevInfo& dev,
                               cudaStream_t s) {
     size_t bytes;
     SortArgs a;
@@ -921,9 +924,14 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, int 
     note_launches(1);
     const int ctas = e.N <= kStaged ? 1 : kSortCtas;
     auto* kernel = ctas == 1 ? embed_sort_kernel<1> : embed_sort_kernel<kSortCtas>;
-    const cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-    if (err != cudaSuccess) return err;
+    static std::atomic<uint64_t> ready[2];  // devices whose kernel has its shared memory
+    const uint64_t bit = uint64_t(1) << dev.device;
+    if (!(ready[ctas == 1].load() & bit)) {
+        const cudaError_t err =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+        if (err != cudaSuccess) return err;
+        ready[ctas == 1].fetch_or(bit);
+    }
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = ctas;
@@ -938,8 +946,9 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, int 
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-cudaError_t launch_embed_bwd(const EmbedArgs& e, int accumulate, void* ws, int num_sms,
+cudaError_t launch_embed_bwd(const EmbedArgs& e, int accumulate, void* ws, const DevInfo& dev,
                              cudaStream_t s) {
+    const int num_sms = dev.num_sms;
     size_t bytes;
     const bool vec = grad_vec(e);
     GradArgs a;
@@ -953,12 +962,16 @@ cudaError_t launch_embed_bwd(const EmbedArgs& e, int accumulate, void* ws, int n
     a.slots = static_cast<int>((e.N + a.K - 1) / a.K);
     a.p = grad_layout(e.N, e.D, e.V, ws, &bytes);
     switch (e.dtype * 3 + e.table_dtype) {
-        case LL_F32 * 3 + LL_F32: return grad_typed<float, float>(e, vec, accumulate, a, num_sms, s);
-        case LL_F16 * 3 + LL_F16: return grad_typed<__half, __half>(e, vec, accumulate, a, num_sms, s);
-        case LL_F16 * 3 + LL_F32: return grad_typed<__half, float>(e, vec, accumulate, a, num_sms, s);
+        case LL_F32 * 3 + LL_F32:
+            return grad_typed<float, float>(e, vec, accumulate, a, num_sms, s);
+        case LL_F16 * 3 + LL_F16:
+            return grad_typed<__half, __half>(e, vec, accumulate, a, num_sms, s);
+        case LL_F16 * 3 + LL_F32:
+            return grad_typed<__half, float>(e, vec, accumulate, a, num_sms, s);
         case LL_BF16 * 3 + LL_BF16:
             return grad_typed<__nv_bfloat16, __nv_bfloat16>(e, vec, accumulate, a, num_sms, s);
-        default: return grad_typed<__nv_bfloat16, float>(e, vec, accumulate, a, num_sms, s);
+        default:
+            return grad_typed<__nv_bfloat16, float>(e, vec, accumulate, a, num_sms, s);
     }
 }
 

@@ -300,9 +300,9 @@ cudaError_t launch_embed_fwd(const EmbedArgs& a, cudaStream_t s);
 size_t embed_bwd_bytes(int64_t N, int64_t D, int64_t V);
 // The gradient's two launches, in this order: the tokens sorted into the
 // workspace (and, without accumulate, rows of no token set to +0), then the sums.
-cudaError_t launch_embed_sort(const EmbedArgs& a, int accumulate, void* ws, int num_sms,
+cudaError_t launch_embed_sort(const EmbedArgs& a, int accumulate, void* ws, const DevInfo& dev,
                               cudaStream_t s);
-cudaError_t launch_embed_bwd(const EmbedArgs& a, int accumulate, void* ws, int num_sms,
+cudaError_t launch_embed_bwd(const EmbedArgs& a, int accumulate, void* ws, const DevInfo& dev,
                              cudaStream_t s);
 
 // --- policy loss (policy_kernels.cu) -------------------------------------------
