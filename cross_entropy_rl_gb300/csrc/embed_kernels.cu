@@ -144,7 +144,10 @@ struct SortHead {
 
 struct SortPtrs {
     SortHead* head;
-    unsigned long long *buf0, *buf1;  // [N] (row << 32 | position)
+    // of more tokens than a cluster sorts
+    unsigned long long *buf0, *buf1;  // [N] keys
+    int *counts, *totals;             // [kBins, blocks of kStaged], [kBins]
+    uint16_t* places;                 // [N]
     Entry* entries;                   // [N]
     int* windows;                     // [ceil(N / window) + 1] start of the unit of each
                                       // window-th entry
@@ -165,6 +168,7 @@ struct SortArgs {
     char* table;
     int64_t row_bytes, pitch;
     float now;  // share of the rows that is filled beside the sort
+    bool mark;  // the sort itself marks the rows of tokens as used
 };
 
 extern __shared__ __align__(16) unsigned char sort_smem[];
@@ -202,33 +206,181 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
     return s - x;
 }
 
+typedef unsigned long long Key;  // row << 32 | position
+constexpr Key kNone = ~0ull;     // no token of the table
+
+__device__ __forceinline__ Key key_of(const SortArgs& a, int64_t i, int64_t y) {
+    const int64_t v = y - a.v0;
+    if (y < a.v0 || v >= a.V) return kNone;
+    return static_cast<Key>(v) << 32 | static_cast<unsigned>(i);
+}
+
+// Digits of a sorting pass: `bins` values from bit `shift` of the row on.
+struct Digits {
+    int shift, bins;
+    __device__ __forceinline__ Digits(const SortArgs& a, int pass) : shift(0) {
+        for (int p = 0;; ++p) {
+            const int bits = (a.bits - shift + (a.passes - p) - 1) / (a.passes - p);
+            bins = 1 << bits;
+            if (p == pass) break;
+            shift += bits;
+        }
+    }
+    __device__ __forceinline__ int of(Key k) const {
+        return k == kNone ? -1 : static_cast<int>(k >> (32 + shift)) & (bins - 1);
+    }
+};
+
+// Counts a warp's keys by digit.  The lanes of equal digit find each other by
+// setting their bits in the digit's word of the warp (a vote for each bit of the
+// digit took 4x the time, match.any more), and one of them counts for all.
+struct WarpCounts {
+    int* count;      // [bins]
+    unsigned* word;  // [bins], 0 between the calls
+    // A key's place among the warp's keys of its digit so far (d = -1: no key).
+    __device__ __forceinline__ int add(int d) {
+        const int lane = threadIdx.x & 31;
+        const unsigned under = (1u << lane) - 1;
+        if (d >= 0) atomicOr(word + d, 1u << lane);
+        __syncwarp();
+        const unsigned peers = d >= 0 ? word[d] : 0;
+        const int had = d >= 0 ? count[d] : 0;
+        __syncwarp();
+        if (d >= 0 && (peers & under) == 0) {
+            count[d] = had + __popc(peers);
+            word[d] = 0;
+        }
+        __syncwarp();
+        return had + __popc(peers & under);
+    }
+};
+
+// counts [kSortWarps][bins]: each warp's become those of the warps below it; the
+// sum over the warps of thread tid's digit comes back.
+__device__ __forceinline__ int sum_over_warps(int* counts, int bins) {
+    int sum = 0;
+    if (threadIdx.x >= bins) return 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        const int c = counts[w * bins + threadIdx.x];
+        counts[w * bins + threadIdx.x] = sum;
+        sum += c;
+    }
+    return sum;
+}
+
+// Exclusive sum of x over the block's threads; `all` is the sum of all.
+__device__ __forceinline__ int block_scan(int x, int& all) {
+    __shared__ int scan[kSortWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int low = warp_scan(x, lane);
+    __syncthreads();
+    if (lane == 31) scan[warp] = low + x;
+    __syncthreads();
+    int under = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        if (w < warp) under += scan[w];
+        all += scan[w];
+    }
+    return under + low;
+}
+
+// The sorted keys [beg, end) of a warp: heads[r] are the lanes that start a token
+// in round r of the block at i (the lane's first).  `prev` is the row ahead of the
+// block, and then its last row.
+__device__ __forceinline__ void heads_of(const Key (&k)[kRounds], int64_t i, int64_t end,
+                                         unsigned& prev, unsigned (&heads)[kRounds]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const unsigned row = static_cast<unsigned>(k[r] >> 32);
+        const unsigned up = __shfl_up_sync(0xffffffffu, row, 1);
+        const bool differs = row != (lane == 0 ? prev : up);
+        heads[r] = __ballot_sync(0xffffffffu, i + r * 32 < end && differs);
+        prev = __shfl_sync(0xffffffffu, row, 31);
+    }
+}
+
+// Entries of the sorted keys [beg, end) of a warp, with their units' ends.
+// `head` is where the token that the run starts inside started (any value if it
+// starts with one), before and after the rows next to the run (~0: none).
+// block(i, k) gives kRounds rounds of keys, kNone from `end` on; key_at(i) one.
+template <typename B, typename K>
+__device__ __forceinline__ void write_entries(const SortArgs& a, int64_t beg, int64_t end, int head,
+                                              unsigned before, unsigned after, const B& block,
+                                              const K& key_at) {
+    const int lane = threadIdx.x & 31;
+    const unsigned upto = ~0u >> (31 - lane);  // lanes up to this one
+    const int mask = a.K - 1;                  // K is a power of two
+#pragma unroll 1
+    for (int64_t i0 = beg + lane; i0 - lane < end; i0 += 32 * kRounds) {
+        Key k[kRounds];
+        unsigned heads[kRounds];
+        block(i0, k);
+        heads_of(k, i0, end, before, heads);
+        const int64_t i1 = i0 - lane + 32 * kRounds;
+        unsigned beyond = after;  // the row after the block
+        if (i1 < end) beyond = static_cast<unsigned>(key_at(i1) >> 32);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int i = static_cast<int>(i0) + r * 32, b = i - lane;
+            const unsigned row = static_cast<unsigned>(k[r] >> 32);
+            const unsigned down = __shfl_down_sync(0xffffffffu, row, 1);
+            const unsigned up = static_cast<unsigned>(k[(r + 1) % kRounds] >> 32);
+            const unsigned first = r + 1 < kRounds ? __shfl_sync(0xffffffffu, up, 0) : beyond;
+            const unsigned seen = heads[r] & upto;
+            const int h = seen ? b + 31 - __clz(seen) : head;
+            if (i < end) {
+                const unsigned next = i + 1 == end ? after : lane == 31 ? first : down;
+                const int in = (i - h) & mask;  // place in its unit
+                const bool token_ends = row != next;
+                const bool unit_ends = token_ends || in == mask;
+                const bool more = unit_ends && (i - h >= a.K || !token_ends);
+                a.p.entries[i] = Entry{static_cast<unsigned>(k[r]) | (unit_ends ? kTop : 0u),
+                                       row | (more ? kTop : 0u)};
+                if (i % a.window == 0) a.p.windows[i / a.window] = i - in;
+                if (a.mark && token_ends) atomicOr(a.p.used + row / 32, 1u << row % 32);
+                if (token_ends && i - h >= a.K) {
+                    const bool huge = i - h >= a.K * kFewPieces;
+                    const int at = atomicAdd(huge ? &a.p.head->huges : &a.p.head->longs, 1);
+                    a.p.longs[huge ? a.slots - 1 - at : at] =
+                        Long{h, i + 1 - h, static_cast<int>(row), 0};
+                }
+            }
+            if (heads[r]) head = b + 31 - __clz(heads[r]);
+        }
+    }
+}
+
+__device__ __forceinline__ void write_head(const SortArgs& a, int64_t M) {
+    a.p.head->valid = static_cast<int>(M);
+    a.p.windows[(M + a.window - 1) / a.window] = static_cast<int>(M);
+}
+
 // Least-significant-digit radix sort by one CTA or one cluster, stable, so that
 // the positions of a token stay ascending.  Each warp owns a run of the keys; a
 // pass counts the run's digits, scans the counts over warps, CTAs and digits,
-// and writes each key to its place.  The lanes of equal digit find each other by
-// setting their bits in the digit's word of the warp (a vote for each bit of the
-// digit took 4x the time, match.any more), and one of them counts for all.
-// Tokens outside the table drop out in the first pass.  Up to kStaged keys a CTA
-// stay in shared memory: a CTA's runs lie side by side there, and a key goes to
-// its place in the other buffer of the CTA whose run that is.  The loops are kept
-// short: the sort is some ten thousand cycles long and its instructions are
-// fetched cold (eight rounds unrolled, counting 300 tokens took 3.2k cycles
-// instead of 0.9k).  300 / 4096 / 32768 tokens: 6 / 12 / 21 us.
+// and writes each key to its place.  Tokens outside the table drop out in the
+// first pass.  The keys stay in shared memory: a CTA's runs lie side by side
+// there, and a key goes to its place in the other buffer of the CTA whose run that
+// is.  The loops are kept short: the sort is some ten thousand cycles long and its
+// instructions are fetched cold (eight rounds unrolled, counting 300 tokens took
+// 3.2k cycles instead of 0.9k).  300 / 4096 / 32768 tokens: 6 / 12 / 21 us.
 template <int CTAS>
 __device__ void sort_tokens(const SortArgs& a) {
-    typedef unsigned long long Key;
-    constexpr Key kNone = ~0ull;
     int* hist = reinterpret_cast<int*>(sort_smem);  // [kSortWarps][bins]
     Key* keys = reinterpret_cast<Key*>(sort_smem + kSortWarps * kBins * 4);
+    Key* other = keys + kStaged;  // keys of the next pass
     uint16_t* places = reinterpret_cast<uint16_t*>(keys + kStaged * 2);
-    __shared__ int total[kBins], base[kBins], scan[kSortWarps], grand;
+    __shared__ int total[kBins], base[kBins];
     __shared__ int last_head[kSortWarps];
     static_assert(kBins == kSortThreads, "a thread per digit");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = CTAS == 1 ? 0 : cluster_ctarank();
     constexpr int kWarps = CTAS * kSortWarps;
     const int me = rank * kSortWarps + warp;
-    const unsigned lt = (1u << lane) - 1;
     auto all_ctas = [&]() {
         __syncthreads();
         if (CTAS > 1) cluster_barrier();
@@ -237,154 +389,86 @@ __device__ void sort_tokens(const SortArgs& a) {
     // ahead of barriers of all CTAs
     if (rank == 0 && tid == 0) a.p.head->longs = a.p.head->huges = 0;
 
-    int64_t M = a.N, beg, end;
-    const bool staged = CTAS == 1 || M <= CTAS * kStaged;
-    unsigned run;   // keys of a warp
-    Key* mine;      // the warp's staged keys
+    int M = static_cast<int>(a.N), beg, end;
+    unsigned run;  // keys of a warp
     auto set_run = [&]() {
-        const int64_t per = ((M + 31) / 32 + kWarps - 1) / kWarps * 32;
-        beg = me * per < M ? me * per : M;
-        end = beg + per < M ? beg + per : M;
-        run = static_cast<unsigned>(per);
-        mine = keys + warp * per;
-    };
-    // Sorted keys of the passes, alternately in two buffers; ahead of the first,
-    // keys made of the tokens.
-    const Key* src = nullptr;
-    Key* dst = a.p.buf0;
-    Key* other = keys + kStaged;  // staged keys of the next pass
-    auto key_of = [&](int64_t i, int64_t y) -> Key {
-        const int64_t v = y - a.v0;
-        if (y < a.v0 || v >= a.V) return kNone;
-        return static_cast<Key>(v) << 32 | static_cast<unsigned>(i);
-    };
-    auto source = [&](int64_t i) {
-        return src ? __ldcg(src + i) : key_of(i, a.tokens[i]);
-    };
-    auto stage = [&]() {
-        if (beg >= end) return;
-        int64_t y[kWarpStaged / 32];
-#pragma unroll
-        for (int q = 0; q < kWarpStaged / 32; ++q) {
-            const int64_t i = beg + q * 32 + lane;
-            y[q] = __ldcg(a.tokens + (i < end ? i : end - 1));
-        }
-#pragma unroll
-        for (int q = 0; q < kWarpStaged / 32; ++q) {
-            const int64_t i = beg + q * 32 + lane;
-            if (i < end) mine[q * 32 + lane] = key_of(i, y[q]);
-        }
+        run = ((M + 31) / 32 + kWarps - 1) / kWarps * 32;
+        beg = min(me * static_cast<int>(run), M);
+        end = min(beg + static_cast<int>(run), M);
     };
     // Keys of kRounds rounds from i on, i the lane's first.
     auto block = [&](int64_t i, Key (&k)[kRounds]) {
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             const int64_t at = i + r * 32;
-            k[r] = at >= end ? kNone : staged ? mine[at - beg] : source(at);
+            k[r] = at >= end ? kNone : keys[warp * run + (at - beg)];
         }
     };
-
-    int shift = 0;
+    set_run();
+    if (beg < end) {
+        int64_t y[kWarpStaged / 32];
+#pragma unroll
+        for (int q = 0; q < kWarpStaged / 32; ++q)
+            y[q] = __ldcg(a.tokens + min(beg + q * 32 + lane, end - 1));
+#pragma unroll
+        for (int q = 0; q < kWarpStaged / 32; ++q) {
+            const int i = beg + q * 32 + lane;
+            if (i < end) keys[warp * run + q * 32 + lane] = key_of(a, i, y[q]);
+        }
+    }
     for (int pass = 0; pass < a.passes; ++pass) {
-        const int db = (a.bits - shift + (a.passes - pass) - 1) / (a.passes - pass);
-        const int bins = 1 << db;
+        const Digits digits(a, pass);
+        const int bins = digits.bins;
         set_run();
-        if (staged && pass == 0) stage();
-        unsigned* words = reinterpret_cast<unsigned*>(other);
+        unsigned* words = reinterpret_cast<unsigned*>(other);  // empty as yet
         for (int i = tid; i < kSortWarps * bins; i += kSortThreads) hist[i] = words[i] = 0;
         __syncthreads();
         int* count = hist + warp * bins;
-        unsigned* word = words + warp * bins;
-        // A lane's place among the keys of its digit so far; counts the digits.
-        auto place = [&](int d) {
-            if (d >= 0) atomicOr(word + d, 1u << lane);
-            __syncwarp();
-            const unsigned peers = d >= 0 ? word[d] : 0;
-            const int had = d >= 0 ? count[d] : 0;
-            __syncwarp();
-            if (d >= 0 && (peers & lt) == 0) {
-                count[d] = had + __popc(peers);
-                word[d] = 0;
-            }
-            __syncwarp();
-            return had + __popc(peers & lt);
-        };
-        auto digit = [&](Key k) {
-            return k == kNone ? -1 : static_cast<int>(k >> (32 + shift)) & (bins - 1);
-        };
-        const int place0 = static_cast<int>((mine - keys) % kStaged - beg);
+        WarpCounts counts{count, words + warp * bins};
+        uint16_t* place = places + warp * run - beg;
 #pragma unroll 1
-        for (int64_t i = beg + lane; i - lane < end; i += 32 * kRounds) {
+        for (int i = beg + lane; i - lane < end; i += 32 * kRounds) {
             Key k[kRounds];
-            int d[kRounds];
             block(i, k);
 #pragma unroll
-            for (int r = 0; r < kRounds; ++r) d[r] = digit(k[r]);
-#pragma unroll
             for (int r = 0; r < kRounds; ++r) {
-                const int at = place(d[r]);
-                if (staged && d[r] >= 0) places[place0 + i + r * 32] = at;
+                const int at = counts.add(digits.of(k[r]));
+                if (i + r * 32 < end) place[i + r * 32] = at;
             }
         }
         __syncthreads();
-        if (tid < bins) {  // counts of the warps below, and of the CTA
-            int sum = 0;
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) {
-                const int c = hist[w * bins + tid];
-                hist[w * bins + tid] = sum;
-                sum += c;
-            }
-            total[tid] = sum;
-        }
+        const int mine = sum_over_warps(hist, bins);
+        if (tid < bins) total[tid] = mine;
         all_ctas();
         int before = 0, all = 0;
         if (tid < bins) {
 #pragma unroll
             for (uint32_t r = 0; r < CTAS; ++r) {
-                const int c = CTAS == 1 ? total[tid] : ld_cluster(total + tid, r);
-                if (r < rank) before += c;
+                const int c = CTAS == 1 ? mine : ld_cluster(total + tid, r);
+                if (CTAS > 1 && r < rank) before += c;
                 all += c;
             }
         }
-        const int low = warp_scan(all, lane);  // digits below, within 32
-        if (lane == 31) scan[warp] = low + all;
-        __syncthreads();
-        int under = 0, sum = 0;  // digits of the warps below
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
-            if (w < warp) under += scan[w];
-            sum += scan[w];
-        }
-        if (tid < bins) base[tid] = under + low + before;
-        if (tid == 0) grand = sum;
+        int grand;
+        const int low = block_scan(all, grand);
+        if (tid < bins) base[tid] = low + before;
         __syncthreads();
         if (pass == 0) M = grand;
         const unsigned share = ((M + 31) / 32 + kWarps - 1) / kWarps * 32 * kSortWarps;  // of a CTA
 #pragma unroll 1
-        for (int64_t i = beg + lane; i - lane < end; i += 32 * kRounds) {
+        for (int i = beg + lane; i - lane < end; i += 32 * kRounds) {
             Key k[kRounds];
-            int d[kRounds], at[kRounds];
+            int at[kRounds];
             block(i, k);
 #pragma unroll
-            for (int r = 0; r < kRounds; ++r) d[r] = digit(k[r]);
-            if (staged) {
-#pragma unroll
-                for (int r = 0; r < kRounds; ++r)
-                    at[r] = d[r] >= 0 ? count[d[r]] + base[d[r]] + places[place0 + i + r * 32] : 0;
-            } else {
-#pragma unroll
-                for (int r = 0; r < kRounds; ++r) {
-                    const int p = place(d[r]);
-                    at[r] = d[r] >= 0 ? p + base[d[r]] : 0;
-                }
+            for (int r = 0; r < kRounds; ++r) {
+                const int d = digits.of(k[r]);
+                at[r] = d >= 0 ? count[d] + base[d] + place[i + r * 32] : -1;
             }
 #pragma unroll
             for (int r = 0; r < kRounds; ++r) {
-                if (d[r] < 0) continue;
-                if (!staged) {
-                    dst[at[r]] = k[r];
-                } else if (CTAS == 1) {
+                if (at[r] < 0) continue;
+                if (CTAS == 1) {
                     other[at[r]] = k[r];
                 } else {
                     const unsigned to = static_cast<unsigned>(at[r]) / share;
@@ -392,59 +476,34 @@ __device__ void sort_tokens(const SortArgs& a) {
                 }
             }
         }
-        shift += db;
-        if (staged) {
-            Key* t = keys;
-            keys = other;
-            other = t;
-        } else {
-            src = dst;
-            dst = dst == a.p.buf0 ? a.p.buf1 : a.p.buf0;
-        }
+        Key* t = keys;
+        keys = other;
+        other = t;
         all_ctas();  // every key of the pass is in its place
     }
 
-    // The entries with their units' ends.  All that a warp needs from the runs
-    // ahead of its own is where the last token started.
+    // All that a warp needs from the runs ahead of its own is where the last token
+    // started.
     set_run();
     const unsigned share = run * kSortWarps;
-    auto row_at = [&](int64_t i) -> unsigned {
+    auto row_at = [&](int i) -> unsigned {
         if (i < 0 || i >= M) return ~0u;
-        Key k;
-        if (!staged) {
-            k = __ldcg(src + i);
-        } else if (CTAS == 1) {
-            k = keys[i];
-        } else {
-            const unsigned at = static_cast<unsigned>(i) / share;
-            k = ld_cluster64(keys + (i - int64_t(at) * share), at);
-        }
-        return static_cast<unsigned>(k >> 32);
+        const unsigned at = CTAS == 1 ? 0 : static_cast<unsigned>(i) / share;
+        const Key* k = keys + (i - at * share);
+        return static_cast<unsigned>((CTAS == 1 ? *k : ld_cluster64(k, at)) >> 32);
     };
     const unsigned row_before = row_at(beg - 1), row_after = row_at(end);
-    // Lanes of each round that start a token; the row ahead of the block goes in
-    // and the block's last comes out of `prev`.
-    auto heads_of = [&](const Key (&k)[kRounds], int64_t i, unsigned& prev,
-                        unsigned (&heads)[kRounds]) {
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            const unsigned row = static_cast<unsigned>(k[r] >> 32);
-            const unsigned up = __shfl_up_sync(0xffffffffu, row, 1);
-            heads[r] = __ballot_sync(0xffffffffu, i + r * 32 < end && row != (lane == 0 ? prev : up));
-            prev = __shfl_sync(0xffffffffu, row, 31);
-        }
-    };
     int last = -1;
     unsigned prev = row_before;
 #pragma unroll 1
-    for (int64_t i = beg + lane; i - lane < end; i += 32 * kRounds) {
+    for (int i = beg + lane; i - lane < end; i += 32 * kRounds) {
         Key k[kRounds];
         unsigned heads[kRounds];
         block(i, k);
-        heads_of(k, i, prev, heads);
+        heads_of(k, i, end, prev, heads);
 #pragma unroll
         for (int r = 0; r < kRounds; ++r)
-            if (heads[r]) last = static_cast<int>(i) - lane + r * 32 + 31 - __clz(heads[r]);
+            if (heads[r]) last = i - lane + r * 32 + 31 - __clz(heads[r]);
     }
     if (lane == 0) last_head[warp] = last;
     all_ctas();
@@ -459,52 +518,147 @@ __device__ void sort_tokens(const SortArgs& a) {
         }
     }
     head = __reduce_max_sync(0xffffffffu, head);
-    prev = row_before;
-    const int mask = a.K - 1;  // K is a power of two
+    write_entries(a, beg, end, head, row_before, row_after, block,
+                  [&](int64_t i) { return keys[warp * run + (i - beg)]; });
+    if (rank == 0 && tid == 0) write_head(a, M);
+    all_ctas();  // no CTA leaves while another reads its shared memory
+}
+
+// More tokens than a cluster holds: the same sort over the whole device, three
+// launches a pass and one for the entries.  A block owns kStaged keys.
+// 131072 / 1000003 tokens: 38 / 58 us; the cluster, its keys in L2, took 87 / 585.
+struct BigSort {
+    const Key* src;    // nullptr: keys made of the tokens (the first pass)
+    Key* dst;
+    int* counts;       // [kBins][blocks]: keys of a digit, then of the blocks below
+    int* totals;       // [kBins]
+    uint16_t* places;  // [N] place among the block's keys of its digit
+    int64_t blocks;
+    int pass;
+};
+constexpr uint16_t kNoPlace = 0xffff;
+constexpr int kCountSmem = kSortWarps * kBins * 8 + kStaged * 4;
+
+__device__ __forceinline__ Key big_key(const SortArgs& a, const BigSort& s, int64_t i) {
+    return s.src ? __ldcg(s.src + i) : key_of(a, i, a.tokens[i]);
+}
+__device__ __forceinline__ int64_t big_keys(const SortArgs& a, const BigSort& s) {
+    return s.pass == 0 ? a.N : a.p.head->valid;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 2)
+    embed_count_kernel(const __grid_constant__ SortArgs a, const __grid_constant__ BigSort s) {
+    int* hist = reinterpret_cast<int*>(sort_smem);
+    unsigned* words = reinterpret_cast<unsigned*>(hist + kSortWarps * kBins);
+    unsigned* found = words + kSortWarps * kBins;  // [kStaged] place << kDigitBits | digit
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    wait_for_prerequisites();
+    launch_dependents();
+    const Digits digits(a, s.pass);
+    const int bins = digits.bins;
+    for (int i = tid; i < kSortWarps * bins; i += kSortThreads) hist[i] = words[i] = 0;
+    __syncthreads();
+    const int64_t M = big_keys(a, s), b0 = int64_t(blockIdx.x) * kStaged;
+    WarpCounts counts{hist + warp * bins, words + warp * bins};
 #pragma unroll 1
-    for (int64_t i0 = beg + lane; i0 - lane < end; i0 += 32 * kRounds) {
+    for (int j = warp * kWarpStaged + lane; j < (warp + 1) * kWarpStaged; j += 32 * kRounds) {
         Key k[kRounds];
-        unsigned heads[kRounds];
-        block(i0, k);
-        heads_of(k, i0, prev, heads);
-        // the row after the block
-        const int64_t i1 = i0 - lane + 32 * kRounds;
-        unsigned beyond = row_after;
-        if (i1 < end)
-            beyond = static_cast<unsigned>((staged ? mine[i1 - beg] : source(i1)) >> 32);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+            k[r] = b0 + j + r * 32 < M ? big_key(a, s, b0 + j + r * 32) : kNone;
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
-            const int i = static_cast<int>(i0) + r * 32, b = i - lane;
-            const unsigned row = static_cast<unsigned>(k[r] >> 32);
-            const unsigned down = __shfl_down_sync(0xffffffffu, row, 1);
-            const unsigned up = static_cast<unsigned>(k[(r + 1) % kRounds] >> 32);
-            const unsigned first = r + 1 < kRounds ? __shfl_sync(0xffffffffu, up, 0) : beyond;
-            const unsigned upto = heads[r] & (lt | (1u << lane));
-            const int h = upto ? b + 31 - __clz(upto) : head;
-            if (i < end) {
-                const unsigned next = i + 1 == end ? row_after : lane == 31 ? first : down;
-                const int in = (i - h) & mask;  // place in its unit
-                const bool token_ends = row != next;
-                const bool unit_ends = token_ends || in == mask;
-                const bool more = unit_ends && (i - h >= a.K || !token_ends);
-                a.p.entries[i] = Entry{static_cast<unsigned>(k[r]) | (unit_ends ? kTop : 0u),
-                                       row | (more ? kTop : 0u)};
-                if (i % a.window == 0) a.p.windows[i / a.window] = i - in;
-                if (token_ends && i - h >= a.K) {
-                    const bool huge = i - h >= a.K * kFewPieces;
-                    const int at = atomicAdd(huge ? &a.p.head->huges : &a.p.head->longs, 1);
-                    a.p.longs[huge ? a.slots - 1 - at : at] =
-                        Long{h, i + 1 - h, static_cast<int>(row), 0};
-                }
-            }
-            if (heads[r]) head = b + 31 - __clz(heads[r]);
+            const int d = digits.of(k[r]);
+            const int at = counts.add(d);
+            found[j + r * 32] = d < 0 ? ~0u : static_cast<unsigned>(at << kDigitBits | d);
         }
     }
-    if (rank == 0 && tid == 0) {
-        a.p.head->valid = static_cast<int>(M);
-        a.p.windows[(M + a.window - 1) / a.window] = static_cast<int>(M);
+    __syncthreads();
+    const int sum = sum_over_warps(hist, bins);
+    if (tid < bins) s.counts[tid * s.blocks + blockIdx.x] = sum;
+    __syncthreads();
+    for (int j = warp * kWarpStaged + lane; j < (warp + 1) * kWarpStaged; j += 32) {
+        const unsigned f = found[j];
+        if (b0 + j < M)
+            s.places[b0 + j] = f == ~0u ? kNoPlace
+                                        : hist[warp * bins + (f & (kBins - 1))] + (f >> kDigitBits);
     }
-    all_ctas();  // no CTA leaves while another reads its shared memory
+}
+
+// A digit's counts become those of the blocks below.
+__global__ void __launch_bounds__(kSortThreads)
+    embed_scan_kernel(const __grid_constant__ BigSort s) {
+    wait_for_prerequisites();
+    launch_dependents();
+    int* row = s.counts + blockIdx.x * s.blocks;
+    int sum = 0;
+    for (int64_t b = 0; b < s.blocks; b += kSortThreads) {
+        const int c = b + threadIdx.x < s.blocks ? row[b + threadIdx.x] : 0;
+        int all;
+        const int under = block_scan(c, all);
+        if (b + threadIdx.x < s.blocks) row[b + threadIdx.x] = sum + under;
+        sum += all;
+    }
+    if (threadIdx.x == 0) s.totals[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    embed_place_kernel(const __grid_constant__ SortArgs a, const __grid_constant__ BigSort s) {
+    __shared__ int base[kBins];
+    const int tid = threadIdx.x;
+    wait_for_prerequisites();
+    launch_dependents();
+    const Digits digits(a, s.pass);
+    int all;
+    const int low = block_scan(tid < digits.bins ? s.totals[tid] : 0, all);
+    if (tid < digits.bins) base[tid] = low + s.counts[tid * s.blocks + blockIdx.x];
+    const int64_t M = big_keys(a, s), b0 = int64_t(blockIdx.x) * kStaged;
+    __syncthreads();
+#pragma unroll 4
+    for (int j = tid; j < kStaged; j += kSortThreads) {
+        if (b0 + j >= M) break;
+        const int p = s.places[b0 + j];
+        if (p == kNoPlace) continue;
+        const Key k = big_key(a, s, b0 + j);
+        s.dst[base[digits.of(k)] + p] = k;
+    }
+    if (s.pass == 0 && blockIdx.x == 0 && tid == 0) {
+        a.p.head->longs = a.p.head->huges = 0;
+        write_head(a, all);
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    embed_entries_kernel(const __grid_constant__ SortArgs a, const Key* __restrict__ key) {
+    const int lane = threadIdx.x & 31;
+    wait_for_prerequisites();
+    launch_dependents();
+    const int64_t M = a.p.head->valid;
+    const int64_t beg = blockIdx.x * int64_t(kStaged) + (threadIdx.x >> 5) * kWarpStaged;
+    if (beg >= M) return;
+    const int64_t end = beg + kWarpStaged < M ? beg + kWarpStaged : M;
+    auto row_at = [&](int64_t i) { return static_cast<unsigned>(key[i] >> 32); };
+    const unsigned row = row_at(beg), before = beg > 0 ? row_at(beg - 1) : ~0u;
+    int64_t lo = beg;  // where the run's first token started: 32 probes a step
+    if (row == before) {
+        lo = 0;
+        int64_t hi = beg - 1;  // the row at hi is the token's
+        while (lo < hi) {
+            const int64_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+            const bool less = at < hi && row_at(at) < row;
+            const int n = __popc(__ballot_sync(0xffffffffu, less));
+            if (n == 0) break;
+            const int64_t p = lo + (n - 1) * step;
+            lo = p + 1;
+            hi = p + step < hi ? p + step : hi;
+        }
+    }
+    auto block = [&](int64_t i, Key (&k)[kRounds]) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) k[r] = i + r * 32 < end ? key[i + r * 32] : kNone;
+    };
+    write_entries(a, beg, end, static_cast<int>(lo), before, end < M ? row_at(end) : ~0u, block,
+                  [&](int64_t i) { return key[i]; });
 }
 
 // [p, p + bytes) set to +0 by thread `me` of `threads`.
@@ -634,9 +788,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, ADD ? 3 : 4) embed_grad_kerne
         block = block < 2 * turns ? block >> 1 : block - turns;
         if (fill) {
             const int64_t v0 = block * a.fill_rows;
+            const int rows = static_cast<int>(a.V - v0 < a.fill_rows ? a.V - v0 : a.fill_rows);
             fill_rows_of(reinterpret_cast<char*>(dW + v0 * a.ldw), a.ldw * int64_t(sizeof(TO)),
-                         a.row_bytes, static_cast<int>(a.V - v0 < a.fill_rows ? a.V - v0 : a.fill_rows),
-                         a.p.used[v0 / 32] >> (v0 % 32), threadIdx.x, 32 * kGradWarps);
+                         a.row_bytes, rows, a.p.used[v0 / 32] >> (v0 % 32), threadIdx.x, 32 * kGradWarps);
             return;
         }
     }
@@ -828,9 +982,9 @@ cudaError_t grad_typed(const EmbedArgs& e, bool vec, int accumulate, GradArgs a,
     auto run = [&](auto* sums, auto* join) {
         note_launches(join_blocks ? 2 : 1);
         const cudaError_t err =
-            launch_after(sums, static_cast<unsigned>(blocks), threads, s, g, dW, a);
+            launch_after(sums, static_cast<unsigned>(blocks), threads, s, 0, g, dW, a);
         if (err != cudaSuccess || !join_blocks) return err;
-        return launch_after(join, join_blocks, threads, s, dW, a);
+        return launch_after(join, join_blocks, threads, s, 0, dW, a);
     };
     constexpr int R = kGradRows;
     if (vec)
@@ -874,8 +1028,12 @@ static SortPtrs grad_layout(int64_t N, int64_t D, int64_t V, void* ws, size_t* b
     SortPtrs q;
     q.Dp = (D + 7) / 8 * 8;
     q.head = reinterpret_cast<SortHead*>(take(sizeof(SortHead)));
-    q.buf0 = reinterpret_cast<unsigned long long*>(take(size_t(N) * 8));
-    q.buf1 = reinterpret_cast<unsigned long long*>(take(size_t(N) * 8));
+    const int64_t big = N > kStaged * kSortCtas ? N : 0;
+    q.buf0 = reinterpret_cast<unsigned long long*>(take(size_t(big) * 8));
+    q.buf1 = reinterpret_cast<unsigned long long*>(take(size_t(big) * 8));
+    q.counts = reinterpret_cast<int*>(take(size_t((big + kStaged - 1) / kStaged) * kBins * 4));
+    q.totals = reinterpret_cast<int*>(take(big ? kBins * 4 : 0));
+    q.places = reinterpret_cast<uint16_t*>(take(size_t(big) * 2));
     q.entries = reinterpret_cast<Entry*>(take(size_t(N) * sizeof(Entry)));
     const int64_t w = window_rows(N);
     q.windows = reinterpret_cast<int*>(take(size_t((N + w - 1) / w + 1) * 4));
@@ -898,6 +1056,48 @@ static int bits_of(int64_t V) {
     return b;
 }
 
+// Lets a kernel have `bytes` of dynamic shared memory, once on a device.
+template <typename F>
+static cudaError_t give_smem(F* kernel, int bytes, const DevInfo& dev,
+                             std::atomic<uint64_t>& ready) {
+    const uint64_t bit = uint64_t(1) << dev.device;
+    if (ready.load() & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit);
+    return e;
+}
+
+static cudaError_t launch_big_sort(const SortArgs& a, const DevInfo& dev, cudaStream_t s) {
+    static std::atomic<uint64_t> ready;
+    cudaError_t e = give_smem(embed_count_kernel, kCountSmem, dev, ready);
+    if (e == cudaSuccess && a.table)
+        e = cudaMemsetAsync(a.p.used, 0, size_t((a.V + 31) / 32) * 4, s);
+    BigSort b{nullptr, a.p.buf0, a.p.counts, a.p.totals, a.p.places,
+              (a.N + kStaged - 1) / kStaged, 0};
+    const unsigned blocks = static_cast<unsigned>(b.blocks);
+    int bits = a.bits;
+    for (; e == cudaSuccess && b.pass < a.passes; ++b.pass) {
+        const int db = (bits + (a.passes - b.pass) - 1) / (a.passes - b.pass);
+        bits -= db;
+        note_launches(3);
+        if (b.pass == 0) {  // whatever is ahead of it
+            embed_count_kernel<<<blocks, kSortThreads, kCountSmem, s>>>(a, b);
+            e = cudaGetLastError();
+        } else {
+            e = launch_after(embed_count_kernel, blocks, kSortThreads, s, kCountSmem, a, b);
+        }
+        if (e == cudaSuccess) e = launch_after(embed_scan_kernel, 1u << db, kSortThreads, s, 0, b);
+        if (e == cudaSuccess)
+            e = launch_after(embed_place_kernel, blocks, kSortThreads, s, 0, a, b);
+        b.src = b.dst;
+        b.dst = b.dst == a.p.buf0 ? a.p.buf1 : a.p.buf0;
+    }
+    if (e != cudaSuccess) return e;
+    note_launches(1);
+    return launch_after(embed_entries_kernel, blocks, kSortThreads, s, 0, a, b.src);
+}
+
 cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, const DevInfo& dev,
                               cudaStream_t s) {
     size_t bytes;
@@ -916,6 +1116,9 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, cons
     a.table = accumulate ? nullptr : static_cast<char*>(e.table);
     a.row_bytes = e.D * es;
     a.pitch = e.ld_table * es;
+    a.now = 0.f;
+    a.mark = e.N > kStaged * kSortCtas && !accumulate;
+    if (e.N > kStaged * kSortCtas) return launch_big_sort(a, dev, s);
     // The sort takes about 10 us and 0.3 us per thousand tokens.
     const double beside = 48e6 + 1600.0 * static_cast<double>(e.N);
     const double total = static_cast<double>(e.V) * static_cast<double>(a.row_bytes);
@@ -924,14 +1127,9 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, cons
     note_launches(1);
     const int ctas = e.N <= kStaged ? 1 : kSortCtas;
     auto* kernel = ctas == 1 ? embed_sort_kernel<1> : embed_sort_kernel<kSortCtas>;
-    static std::atomic<uint64_t> ready[2];  // devices whose kernel has its shared memory
-    const uint64_t bit = uint64_t(1) << dev.device;
-    if (!(ready[ctas == 1].load() & bit)) {
-        const cudaError_t err =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-        if (err != cudaSuccess) return err;
-        ready[ctas == 1].fetch_or(bit);
-    }
+    static std::atomic<uint64_t> ready[2];
+    const cudaError_t err = give_smem(kernel, kSortSmem, dev, ready[ctas == 1]);
+    if (err != cudaSuccess) return err;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = ctas;

@@ -375,7 +375,7 @@ cudaError_t norm_of(const ll_tensor* t, int64_t count, float* norm, double* part
     });
     if (e != cudaSuccess) return e;
     note_launches(1);
-    return launch_after(grad_norm_kernel, 1, kThreads, s, static_cast<const double*>(part), parts,
+    return launch_after(grad_norm_kernel, 1, kThreads, s, 0, static_cast<const double*>(part), parts,
                         norm);
 }
 
@@ -383,7 +383,7 @@ template <int N>
 cudaError_t clip_by(const ll_tensor* t, int64_t count, float max_norm, const float* norm,
                     int num_sms, cudaStream_t s) {
     return each_list<N>(t, count, num_sms, [&](const GradList<N>& L, unsigned grid) {
-        return launch_after(grad_clip_kernel<N>, grid, kThreads, s, L, norm, max_norm);
+        return launch_after(grad_clip_kernel<N>, grid, kThreads, s, 0, L, norm, max_norm);
     });
 }
 

@@ -332,13 +332,14 @@ __device__ __forceinline__ void launch_dependents() {
 // the stream is done (it calls wait_for_prerequisites()).
 template <typename... P, typename... A>
 inline cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads,
-                                cudaStream_t s, const A&... args) {
+                                cudaStream_t s, unsigned smem, const A&... args) {
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;

@@ -463,7 +463,7 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, void* workspace, cudaStream_
     const int64_t blocks = (a.N + kThreads - 1) / kThreads;
     const unsigned grid = static_cast<unsigned>(blocks < kPolicyBlocks ? blocks : kPolicyBlocks);
     policy_count_kernel<<<grid, kThreads, 0, s>>>(a, ws, seq_count);
-    return launch_after(policy_loss_kernel, grid, kThreads, s, a, ws,
+    return launch_after(policy_loss_kernel, grid, kThreads, s, 0, a, ws,
                         static_cast<const int*>(seq_count));
 }
 

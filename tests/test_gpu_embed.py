@@ -272,3 +272,25 @@ def test_gradient_where_the_sort_changes(lib, N, V, invalid):
     assert (host64(got[at]) == 1 + want).all()
     got[at] = 1
     assert float(got.min()) == 1 == float(got.max())
+
+
+@pytest.mark.parametrize("N", [3000, 20000, 60000])
+def test_graphs_of_every_sort(lib, N):
+    """A captured call of each kind of sort, replayed on other tokens."""
+    V, D = 5000, 24
+    g = table(N, D, "bf16", 51)
+    y = torch.from_numpy(ids(N, V, 52, 0.3, 0.1)).cuda()
+    dW, dA = torch.empty(V, D, device="cuda"), torch.zeros(V, D, device="cuda")
+    ws = torch.empty(lib.load().ll_embed_workspace_size(N, D, V), dtype=torch.uint8, device="cuda")
+    lib.embed_backward(g, y, V, out=dW, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.embed_backward(g, y, V, out=dW, workspace=ws)
+        lib.embed_backward(g, y, V, out=dA, workspace=ws, accumulate=True)
+    y.copy_(torch.from_numpy(ids(N, V, 53, 0.6, 0.3)).cuda())
+    ws.random_(0, 256)
+    dA.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    want = lib.embed_backward(g, y, V)
+    assert bits_equal(dW, want) and bits_equal(dA, want)
