@@ -1354,11 +1354,12 @@ int ll_policy_loss(const float* logp, const float* old_logp, const float* ref_lo
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (N == 0) return cuda_status(cudaMemsetAsync(stats, 0, 16, s));
     Phase ph("policy_loss", s);
+    const double lo = log1p(-o.clip_low), hi = log1p(o.clip_high);
     return cuda_status(launch_policy_loss(
         PolicyArgs{logp, old_logp, ref_logp, advantages, mask, seq_offsets, n_seqs, N,
-                   log1p(-o.clip_low), log1p(o.clip_high), float(1.0 - o.clip_low),
-                   float(1.0 + o.clip_high), o.kl_coef, o.denominator, float(o.kl_coef), stats,
-                   grad_logp},
+                   {float(lo), float(lo - float(lo))}, {float(hi), float(hi - float(hi))},
+                   float(1.0 - o.clip_low), float(1.0 + o.clip_high), o.kl_coef, o.denominator,
+                   float(o.kl_coef), stats, grad_logp},
         workspace, s));
 }
 

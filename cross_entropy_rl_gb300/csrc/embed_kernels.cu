@@ -3,6 +3,7 @@
 //   forward   out[n, :] = scale * W[y_n - v0, :]  (+0 rows for other tokens)
 //   backward  dW[v, :] (+)= scale * sum_{n: y_n - v0 = v} g[n, :]
 #include <atomic>
+#include <type_traits>
 
 #include "ll_device.cuh"
 
@@ -12,13 +13,14 @@ namespace {
 // ------------------------------------------------------------------- lookup
 // One multiply per element: bound by HBM (a row read, a row written).  A warp
 // takes one row's tile of 32 U chunks of E elements; all its loads are issued
-// before the first store.  32768 x 4096 bf16 of 151936 rows: 59 us, 0.92 of the
-// copy bandwidth (U = 8: 61.5 us).  Rows that do not start on 16-byte boundaries
+// before the first store.  Rows of the output's type with a scale of 1 are copied
+// (COPY).  32768 x 4096 bf16 of 151936 rows: 58 us, 0.94 of the copy bandwidth
+// (scaled 60, U = 2 60, U = 8 67 us).  Rows that do not start on 16-byte boundaries
 // go element by element, U = 16 of them in flight a lane: 10007 x 1001 FP32 to
 // FP16 8.7 us (U = 4: 12.6, 8: 9.3).
 constexpr int kLookupWarps = 8;
 
-template <typename TI, typename TO, int E, int U>
+template <typename TI, typename TO, int E, int U, bool COPY>
 __global__ void __launch_bounds__(32 * kLookupWarps) embed_fwd_kernel(
     const TI* __restrict__ W, int64_t ldw, const int64_t* __restrict__ tokens, int64_t N,
     int64_t D, int64_t V, int64_t v0, float scale, TO* __restrict__ out, int64_t ldo) {
@@ -44,8 +46,12 @@ __global__ void __launch_bounds__(32 * kLookupWarps) embed_fwd_kernel(
             if (c + E <= D) {
                 Pack<TO, E> y;
 #pragma unroll
-                for (int j = 0; j < E; ++j)
-                    y.e[j] = Elem<TO>::from_f(in ? Elem<TI>::to_f(x[u].e[j]) * scale : 0.f);
+                for (int j = 0; j < E; ++j) {
+                    if constexpr (COPY)
+                        y.e[j] = in ? x[u].e[j] : Elem<TO>::from_f(0.f);
+                    else
+                        y.e[j] = Elem<TO>::from_f(in ? Elem<TI>::to_f(x[u].e[j]) * scale : 0.f);
+                }
                 y.store(dst + c);
             } else {
                 for (int64_t i = c; i < D; ++i)
@@ -66,13 +72,15 @@ cudaError_t fwd_typed(const EmbedArgs& a, bool vec, cudaStream_t s) {
                     static_cast<unsigned>(tiles < 65535 ? tiles : 65535));
     const TI* W = static_cast<const TI*>(a.rows);
     TO* out = static_cast<TO*>(a.table);
-    if (vec)
-        embed_fwd_kernel<TI, TO, E, U><<<grid, 32 * kLookupWarps, 0, s>>>(
-            W, a.ld_rows, a.tokens, a.N, a.D, a.V, a.v0, a.scale, out, a.ld_table);
-    else
-        embed_fwd_kernel<TI, TO, 1, U1><<<grid, 32 * kLookupWarps, 0, s>>>(
-            W, a.ld_rows, a.tokens, a.N, a.D, a.V, a.v0, a.scale, out, a.ld_table);
-    return cudaGetLastError();
+    auto run = [&](auto* kernel) {
+        kernel<<<grid, 32 * kLookupWarps, 0, s>>>(W, a.ld_rows, a.tokens, a.N, a.D, a.V, a.v0,
+                                                  a.scale, out, a.ld_table);
+        return cudaGetLastError();
+    };
+    if (!vec) return run(embed_fwd_kernel<TI, TO, 1, U1, false>);
+    constexpr bool kSame = std::is_same_v<TI, TO>;
+    return kSame && a.scale == 1.f ? run(embed_fwd_kernel<TI, TO, E, U, kSame>)
+                                   : run(embed_fwd_kernel<TI, TO, E, U, false>);
 }
 
 bool rows16(const void* p, int64_t ld, size_t es) {
@@ -95,6 +103,9 @@ constexpr int kSortCtas = 8;         // CTAs of the sorting cluster for many tok
 constexpr int kDigitBits = 9;        // most bits of a sorting pass
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kStaged = 4096;        // keys a CTA holds in shared memory
+// Most tokens that one CTA sorts (the sort with nothing to add up: 2048 tokens 12.0
+// us, by the cluster 13.5; 4096 tokens 15.8, by the cluster 14.0).
+constexpr int64_t kOneCta = 2048;
 constexpr int kWarpStaged = kStaged / kSortWarps;
 constexpr int kRounds = 4;           // rounds of 32 keys of a warp at a time
 constexpr int kFillCtas = 256;       // CTAs in all when rows are filled beside the sort
@@ -367,7 +378,7 @@ __device__ __forceinline__ void write_head(const SortArgs& a, int64_t M) {
 // there, and a key goes to its place in the other buffer of the CTA whose run that
 // is.  The loops are kept short: the sort is some ten thousand cycles long and its
 // instructions are fetched cold (eight rounds unrolled, counting 300 tokens took
-// 3.2k cycles instead of 0.9k).  300 / 4096 / 32768 tokens: 6 / 12 / 21 us.
+// 3.2k cycles instead of 0.9k).  300 / 4096 / 32768 tokens: 6 / 11 / 20 us.
 template <int CTAS>
 __device__ void sort_tokens(const SortArgs& a) {
     int* hist = reinterpret_cast<int*>(sort_smem);  // [kSortWarps][bins]
@@ -1125,7 +1136,7 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, cons
     a.now = beside < total ? static_cast<float>(beside / total) : 1.f;
 
     note_launches(1);
-    const int ctas = e.N <= kStaged ? 1 : kSortCtas;
+    const int ctas = e.N <= kOneCta ? 1 : kSortCtas;
     auto* kernel = ctas == 1 ? embed_sort_kernel<1> : embed_sort_kernel<kSortCtas>;
     static std::atomic<uint64_t> ready[2];
     const cudaError_t err = give_smem(kernel, kSortSmem, dev, ready[ctas == 1]);

@@ -311,8 +311,8 @@ struct PolicyArgs {
     const uint8_t* mask;                  // or null
     const int64_t* offs;                  // [n_seqs + 1] or null
     int64_t n_seqs, N;
-    double log_lo, log_hi;     // log(1 - clip_low), log(1 + clip_high)
-    float bound_lo, bound_hi;  // 1 - clip_low, 1 + clip_high
+    float log_lo[2], log_hi[2];  // log(1 - clip_low), log(1 + clip_high): hi, lo parts
+    float bound_lo, bound_hi;    // 1 - clip_low, 1 + clip_high
     double beta_d, denominator;
     float beta;
     float *stats, *grad;

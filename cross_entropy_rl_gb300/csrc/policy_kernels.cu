@@ -109,18 +109,15 @@ __device__ __forceinline__ Exp exp_rests(float d) {
     return {q, d + q};
 }
 
-// delta against a border held in 64 bits.  The FP32 difference is within 2^-24
-// of its magnitude of the exact one, so only a delta next to the border needs
-// the 64-bit difference.
-__device__ __forceinline__ bool above(float delta, float a, float b, double border) {
-    const float f = static_cast<float>(border);
-    if (fabsf(delta - f) > 1e-6f * (1.f + fabsf(f))) return delta > f;
-    return static_cast<double>(a) - static_cast<double>(b) > border;
-}
-__device__ __forceinline__ bool below(float delta, float a, float b, double border) {
-    const float f = static_cast<float>(border);
-    if (fabsf(delta - f) > 1e-6f * (1.f + fabsf(f))) return delta < f;
-    return static_cast<double>(a) - static_cast<double>(b) < border;
+// Whether x - y lies above a border given to about 48 bits: s, the rounded
+// difference, and what its rounding left, against the border's two parts.  (In
+// FP64 next to the border only, the compiler still ran the conversions for every
+// token: that unit was 61% busy.)
+__device__ __forceinline__ bool above(float s, float x, float y, Pair border) {
+    const float t = __fsub_rn(s, x);
+    const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(s, t)), __fadd_rn(y, t));
+    const float rest = finite_or_0(__fsub_rn(e, border.lo), s);
+    return __fadd_rn(__fsub_rn(s, border.hi), rest) > 0.f;
 }
 
 struct Token {
@@ -132,8 +129,9 @@ __device__ __forceinline__ Token token_loss(const PolicyArgs& a, float logp, flo
                                             float A) {
     Token t;
     const float delta = logp - old;
-    t.clipped = A > 0.f ? above(delta, logp, old, a.log_hi)
-                        : (A < 0.f && below(delta, logp, old, a.log_lo));
+    // below the lower border: above it with the signs turned
+    t.clipped = A > 0.f ? above(delta, logp, old, {a.log_hi[0], a.log_hi[1]})
+                        : A < 0.f && above(-delta, old, logp, {-a.log_lo[0], -a.log_lo[1]});
     const float r = expf(delta);
     const float pg = A == 0.f ? 0.f : -A * r;
     t.p = t.clipped ? -A * (A > 0.f ? a.bound_hi : a.bound_lo) : pg;

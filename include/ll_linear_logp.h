@@ -498,8 +498,9 @@ size_t ll_policy_workspace_size(int64_t N, int64_t n_seqs);
  *   stats [4] float, device (written): loss, sum w p, sum w k, sum of w over
  *     the clipped tokens.
  *   grad_logp [N] float, device (written).
- * The clipping border is decided on delta in 64 bits; sums over tokens are
- * held as pairs of FP32 values (about 48 bits) and added in a fixed order.  N == 0 writes stats = 0.
+ * The clipping border is decided on the exact delta; sums over tokens are held
+ * as pairs of FP32 values (about 48 bits) and added in a fixed order.
+ * N == 0 writes stats = 0.
  */
 int ll_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,
                    const float* advantages, const uint8_t* mask, const int64_t* seq_offsets,
