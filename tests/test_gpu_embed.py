@@ -294,3 +294,40 @@ def test_graphs_of_every_sort(lib, N):
     torch.cuda.synchronize()
     want = lib.embed_backward(g, y, V)
     assert bits_equal(dW, want) and bits_equal(dA, want)
+
+
+@pytest.mark.parametrize("dt,out", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("N,D,V,hot", [(1, 4096, 5, 0), (40, 2056, 2, 0), (300, 4096, 9, 0),
+                                       (1023, 1031, 40, 0.3), (1024, 2048, 60, 0),
+                                       (1024, 515, 1, 0), (1025, 2048, 60, 0)])
+def test_few_tokens_added(lib, dt, out, N, D, V, hot):
+    """Few tokens added to a table, most of them many times over: right, and the same
+    bits from every run."""
+    g = table(N, D, dt, 61)
+    y = ids(N, V, 62, hot, invalid=0.05)
+    yc = torch.from_numpy(y).cuda()
+    first = table(V, D, out, 63)
+    start = host64(first)
+    dW = lib.embed_backward(g, yc, V, scale=0.7, accumulate=True, out=first.clone())
+    r, M, c = reference(g, y, V, 0.7, start)
+    check_grad(dW, r, M, c, out)
+    for _ in range(10):
+        assert bits_equal(dW, lib.embed_backward(g, yc, V, scale=0.7, accumulate=True,
+                                                 out=first.clone()))
+
+
+def test_graph_of_few_tokens_added(lib):
+    """A captured call for few tokens, replayed on others."""
+    N, V, D = 700, 500, 136
+    g = table(N, D, "bf16", 71)
+    y = torch.from_numpy(ids(N, V, 72, 0.3, 0.1)).cuda()
+    dA = torch.zeros(V, D, device="cuda")
+    lib.embed_backward(g, y, V, out=dA, accumulate=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.embed_backward(g, y, V, out=dA, accumulate=True)
+    y.copy_(torch.from_numpy(ids(N, V, 73, 0.6, 0.3)).cuda())
+    dA.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bits_equal(dA, lib.embed_backward(g, y, V, out=torch.zeros_like(dA), accumulate=True))
