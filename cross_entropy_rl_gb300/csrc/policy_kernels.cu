@@ -169,14 +169,16 @@ __device__ __forceinline__ int count_tokens(const PolicyArgs& a, const Groups& g
 }
 
 // Unmasked tokens per sequence, and sequences that have one.  Integer atomics:
-// the same counts in any order.
-__device__ __forceinline__ void count_sequences(const PolicyArgs& a, const Groups& g,
+// the same counts in any order.  cleared() is called ahead of every one of them.
+template <typename F>
+__device__ __forceinline__ void count_sequences(const PolicyArgs& a, const Groups& g, const F& cleared,
                                                 PolicyWs* __restrict__ ws,
                                                 int* __restrict__ seq_count) {
     const int lane = threadIdx.x & 31;
     SeqWalk walk;
     int held = -1, count = 0;  // not yet added
     auto flush = [&]() {
+        cleared();
         if (count && lane == 0 && atomicAdd(seq_count + held, count) == 0)
             atomicAdd(&ws->full, 1ull);
         count = 0;
@@ -190,13 +192,14 @@ __device__ __forceinline__ void count_sequences(const PolicyArgs& a, const Group
         const int b = walk.at(a, i * 32, lane);
         if (walk.uniform) {
             const unsigned m = __ballot_sync(0xffffffffu, in && b >= 0);
-            if (b != held) flush();
+            if (b != held && count) flush();
             held = b;
             count += __popc(m);
         } else {
             // one lane adds for all of its sequence
             const int s = in ? b : -1;
             const unsigned peers = __match_any_sync(0xffffffffu, s);
+            cleared();
             if (s >= 0 && lane == __ffs(peers) - 1 && atomicAdd(seq_count + s, __popc(peers)) == 0)
                 atomicAdd(&ws->full, 1ull);
         }
@@ -219,11 +222,12 @@ __device__ __forceinline__ Pair per_token(Pair one, int c) {
 
 // Gradients of a warp's groups; adds to s[0..2] the lane's share of the sums.
 // FP32 sums, unweighted, are over kSlots tokens of one sequence at most.  The
-// next group's tokens are loaded ahead, the first ahead of `counted`, which
-// gives 1 / denominator once the counts are there; the loop is kept small,
-// since in a short call its instructions are fetched cold.
-template <typename F>
-__device__ __forceinline__ void loss_tokens(const PolicyArgs& a, const F& counted,
+// next group's tokens and its sequence's count are loaded ahead, the first's ahead
+// of `counted`, which gives 1 / denominator, and of `ready`, which waits for the
+// counts; the loop is kept small, since in a short call its instructions are
+// fetched cold.
+template <typename R, typename F>
+__device__ __forceinline__ void loss_tokens(const PolicyArgs& a, const R& ready, const F& counted,
                                             const int* __restrict__ seq_count, const Groups& g,
                                             Pair (&s)[3]) {
     const int lane = threadIdx.x & 31;
@@ -239,8 +243,16 @@ __device__ __forceinline__ void loss_tokens(const PolicyArgs& a, const F& counte
         x[3] = a.adv[t];
     };
     fetch(g.beg);
-    const Pair one = counted();
     SeqWalk walk;
+    int b = -1, c = 0;  // sequence and its tokens
+    auto follow = [&](int64_t i) {
+        if (a.offs && i < g.end) b = walk.at(a, i * 32, lane);
+    };
+    auto tokens_of = [&]() { c = b >= 0 ? __ldcg(seq_count + b) : 0; };
+    follow(g.beg);
+    ready();
+    tokens_of();
+    const Pair one = counted();
     int held = -1, slots = 0;
     Pair w = a.offs ? Pair{0.f, 0.f} : one;
     float f[3] = {0.f, 0.f, 0.f};
@@ -259,14 +271,14 @@ __device__ __forceinline__ void loss_tokens(const PolicyArgs& a, const F& counte
         fetch(i + 1);
         const int64_t t = i * 32 + lane;
         if (a.offs) {
-            const int b = walk.at(a, i * 32, lane);
             if (b != held) {
                 if (held >= 0) flush();
                 held = b;
-                const int c = b >= 0 ? __ldcg(seq_count + b) : 0;
                 w = c > 0 ? per_token(one, c) : Pair{0.f, 0.f};
             }
             if (b < 0) use = false;
+            follow(i + 1);
+            if (b != held) tokens_of();
         }
         float grad = 0.f;
         if (use) {
@@ -324,6 +336,15 @@ __device__ __forceinline__ Groups grid_groups(const PolicyArgs& a) {
                   int64_t(gridDim.x) * (kThreads / 32));
 }
 
+__global__ void __launch_bounds__(kThreads) policy_clear_kernel(PolicyWs* __restrict__ ws,
+                                                                int* __restrict__ seq_count,
+                                                                int64_t n_seqs) {
+    launch_dependents();
+    const int64_t i = blockIdx.x * int64_t(kThreads) + threadIdx.x;
+    if (i == 0) ws->full = 0;
+    if (i < n_seqs) seq_count[i] = 0;
+}
+
 __global__ void __launch_bounds__(kThreads) policy_count_kernel(const __grid_constant__ PolicyArgs a,
                                                                 PolicyWs* __restrict__ ws,
                                                                 int* __restrict__ seq_count) {
@@ -331,7 +352,8 @@ __global__ void __launch_bounds__(kThreads) policy_count_kernel(const __grid_con
     launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) ws->done = 0;
     if (a.offs) {
-        count_sequences(a, g, ws, seq_count);
+        count_sequences(a, g, [] { wait_for_prerequisites(); }, ws, seq_count);
+        wait_for_prerequisites();  // of every block, so that the next kernel's wait is for both
     } else {
         __shared__ int all;
         if (threadIdx.x == 0) all = 0;
@@ -350,9 +372,8 @@ __global__ void __launch_bounds__(kThreads, 2) policy_loss_kernel(const __grid_c
     __shared__ Pair one;
     Pair s[3] = {};
     loss_tokens(
-        a,
+        a, [] { wait_for_prerequisites(); },
         [&]() {
-            wait_for_prerequisites();
             if (threadIdx.x < 32) {
                 unsigned long long n = 0;
                 if (a.offs) {
@@ -401,7 +422,7 @@ __global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kSmallThrea
         if (blockIdx.x == 0 && threadIdx.x == 0) ws->full = 0;
         __syncthreads();
         cluster_barrier();
-        count_sequences(a, g, ws, seq_count);
+        count_sequences(a, g, [] {}, ws, seq_count);
         __syncthreads();
         cluster_barrier();
         if (threadIdx.x == 0) one = weight(a, __ldcg(&ws->full));
@@ -428,7 +449,7 @@ __global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kSmallThrea
     }
     __syncthreads();
     Pair s[3] = {};
-    loss_tokens(a, [&]() { return one; }, seq_count, g, s);
+    loss_tokens(a, [] {}, [&]() { return one; }, seq_count, g, s);
     block_sums<kSmallThreads>(s, reinterpret_cast<Pair*>(ws->part) + 3 * blockIdx.x);
     __syncthreads();
     cluster_barrier();
@@ -453,14 +474,17 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, void* workspace, cudaStream_
         policy_small_kernel<<<kSmallCtas, kSmallThreads, 0, s>>>(a, ws, seq_count);
         return cudaGetLastError();
     }
-    note_launches(2);
-    if (a.offs) {
-        const cudaError_t e = cudaMemsetAsync(&ws->full, 0, 16 + size_t(a.n_seqs) * 4, s);
-        if (e != cudaSuccess) return e;
-    }
     const int64_t blocks = (a.N + kThreads - 1) / kThreads;
     const unsigned grid = static_cast<unsigned>(blocks < kPolicyBlocks ? blocks : kPolicyBlocks);
-    policy_count_kernel<<<grid, kThreads, 0, s>>>(a, ws, seq_count);
+    note_launches(a.offs ? 3 : 2);
+    if (a.offs) {
+        const int64_t clear = (a.n_seqs + kThreads - 1) / kThreads;
+        policy_clear_kernel<<<static_cast<unsigned>(clear), kThreads, 0, s>>>(ws, seq_count, a.n_seqs);
+        const cudaError_t e = launch_after(policy_count_kernel, grid, kThreads, s, 0, a, ws, seq_count);
+        if (e != cudaSuccess) return e;
+    } else {
+        policy_count_kernel<<<grid, kThreads, 0, s>>>(a, ws, seq_count);
+    }
     return launch_after(policy_loss_kernel, grid, kThreads, s, 0, a, ws,
                         static_cast<const int*>(seq_count));
 }
