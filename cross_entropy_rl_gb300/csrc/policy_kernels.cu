@@ -31,6 +31,7 @@ struct SeqWalk {
     int base = -2;         // lane l holds the end of sequence base + l; -2: nothing
     int ends = 0;
     bool uniform = false;  // the 32 tokens lie in one sequence
+    int b = -1, until = 0;  // that, and its end (0: more than one)
 
     __device__ __forceinline__ static int offset(const PolicyArgs& a, int64_t i) {
         const int64_t o = a.offs[i];
@@ -49,8 +50,9 @@ struct SeqWalk {
         }
         return lo;
     }
-    __device__ __forceinline__ int at(const PolicyArgs& a, int64_t t64, int lane) {
-        const int t0 = static_cast<int>(t64), t1 = t0 + 31, t = t0 + lane;
+    __device__ __forceinline__ int at(const PolicyArgs& a, int t0, int lane) {
+        const int t1 = t0 + 31, t = t0 + lane;
+        if (t1 < until) return b;  // still inside
         if (base == -2 || __shfl_sync(0xffffffffu, ends, 31) <= t1) {
             base = static_cast<int>(search(a, t0, lane)) - 1;
             const int64_t i = int64_t(base) + 1 + lane;
@@ -59,9 +61,11 @@ struct SeqWalk {
         const unsigned m0 = __ballot_sync(0xffffffffu, ends <= t0);
         const unsigned m1 = __ballot_sync(0xffffffffu, ends <= t1);
         uniform = m0 == m1;
+        until = 0;
         int64_t b;
         if (uniform) {
             b = int64_t(base) + __popc(m0);
+            until = __shfl_sync(0xffffffffu, ends, __popc(m0) & 31);  // of them all: <= t0
         } else if (m1 != ~0u) {
             int n = 0;  // ends <= t
 #pragma unroll
@@ -79,7 +83,8 @@ struct SeqWalk {
             }
             b = lo - 1;
         }
-        return b < a.n_seqs ? static_cast<int>(b) : -1;
+        this->b = b < a.n_seqs ? static_cast<int>(b) : -1;
+        return this->b;
     }
 };
 
@@ -128,13 +133,14 @@ struct Token {
 __device__ __forceinline__ Token token_loss(const PolicyArgs& a, float logp, float old, float ref,
                                             float A) {
     Token t;
-    const float delta = logp - old;
     // below the lower border: above it with the signs turned
-    t.clipped = A > 0.f ? above(delta, logp, old, {a.log_hi[0], a.log_hi[1]})
-                        : A < 0.f && above(-delta, old, logp, {-a.log_lo[0], -a.log_lo[1]});
-    const float r = expf(delta);
+    const bool up = A > 0.f;
+    const float x = up ? logp : old, y = up ? old : logp, s = x - y;
+    t.clipped = above(s, x, y, {up ? a.log_hi[0] : -a.log_lo[0], up ? a.log_hi[1] : -a.log_lo[1]}) &&
+                (up || A < 0.f);
+    const float r = expf(up ? s : -s);
     const float pg = A == 0.f ? 0.f : -A * r;
-    t.p = t.clipped ? -A * (A > 0.f ? a.bound_hi : a.bound_lo) : pg;
+    t.p = t.clipped ? -A * (up ? a.bound_hi : a.bound_lo) : pg;
     t.grad = t.clipped ? 0.f : pg;
     t.k = 0.f;
     if (a.ref) {
@@ -148,15 +154,15 @@ __device__ __forceinline__ Token token_loss(const PolicyArgs& a, float logp, flo
 // Groups of 32 tokens of warp `me` of `warps`: a run, so that a warp walks
 // along the sequences.
 struct Groups {
-    int64_t beg, end;
-    __device__ Groups(int64_t N, int64_t me, int64_t warps) {
-        const int64_t all = (N + 31) / 32, per = (all + warps - 1) / warps;
-        beg = me * per < all ? me * per : all;
-        end = beg + per < all ? beg + per : all;
+    int beg, end;
+    __device__ Groups(int64_t N, int me, int warps) {
+        const int all = static_cast<int>((N + 31) / 32), per = (all + warps - 1) / warps;
+        beg = static_cast<int>(min(int64_t(me) * per, int64_t(all)));
+        end = min(beg + per, all);
     }
 };
 
-__device__ __forceinline__ bool unmasked(const PolicyArgs& a, int64_t t) {
+__device__ __forceinline__ bool unmasked(const PolicyArgs& a, int t) {
     return t < a.N && (!a.mask || a.mask[t]);
 }
 
@@ -164,7 +170,7 @@ __device__ __forceinline__ bool unmasked(const PolicyArgs& a, int64_t t) {
 __device__ __forceinline__ int count_tokens(const PolicyArgs& a, const Groups& g) {
     int n = 0;
 #pragma unroll 4
-    for (int64_t i = g.beg; i < g.end; ++i) n += unmasked(a, i * 32 + (threadIdx.x & 31));
+    for (int i = g.beg; i < g.end; ++i) n += unmasked(a, i * 32 + (threadIdx.x & 31));
     return __reduce_add_sync(0xffffffffu, n);
 }
 
@@ -185,7 +191,7 @@ __device__ __forceinline__ void count_sequences(const PolicyArgs& a, const Group
     };
     bool ahead = unmasked(a, g.beg * 32 + lane), ahead2 = unmasked(a, g.beg * 32 + 32 + lane);
 #pragma unroll 1
-    for (int64_t i = g.beg; i < g.end; ++i) {
+    for (int i = g.beg; i < g.end; ++i) {
         const bool in = ahead;  // the masks of two groups are on their way
         ahead = ahead2;
         ahead2 = unmasked(a, i * 32 + 64 + lane);
@@ -233,8 +239,8 @@ __device__ __forceinline__ void loss_tokens(const PolicyArgs& a, const R& ready,
     const int lane = threadIdx.x & 31;
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     bool in = false;
-    auto fetch = [&](int64_t i) {
-        const int64_t t = i * 32 + lane;
+    auto fetch = [&](int i) {
+        const int t = i * 32 + lane;
         in = i < g.end && unmasked(a, t);
         if (!in) return;
         x[0] = a.logp[t];
@@ -245,7 +251,7 @@ __device__ __forceinline__ void loss_tokens(const PolicyArgs& a, const R& ready,
     fetch(g.beg);
     SeqWalk walk;
     int b = -1, c = 0;  // sequence and its tokens
-    auto follow = [&](int64_t i) {
+    auto follow = [&](int i) {
         if (a.offs && i < g.end) b = walk.at(a, i * 32, lane);
     };
     auto tokens_of = [&]() { c = b >= 0 ? __ldcg(seq_count + b) : 0; };
@@ -265,11 +271,11 @@ __device__ __forceinline__ void loss_tokens(const PolicyArgs& a, const R& ready,
         slots = 0;
     };
 #pragma unroll 1
-    for (int64_t i = g.beg; i < g.end; ++i) {
+    for (int i = g.beg; i < g.end; ++i) {
         const float logp = x[0], old = x[1], ref = x[2], adv = x[3];
         bool use = in;
         fetch(i + 1);
-        const int64_t t = i * 32 + lane;
+        const int t = i * 32 + lane;
         if (a.offs) {
             if (b != held) {
                 if (held >= 0) flush();
@@ -294,17 +300,29 @@ __device__ __forceinline__ void loss_tokens(const PolicyArgs& a, const R& ready,
     flush();
 }
 
+// Sums of a warp's s[0..2]: lane 0 gets the first, 16 the second, 8 the third.  The
+// lanes share out the values as they go: 6 additions instead of 15.
+__device__ __forceinline__ Pair warp_sums(const Pair (&s)[3]) {
+    auto other = [](Pair x, int o) {
+        return Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
+    };
+    const bool b16 = threadIdx.x & 16, b8 = threadIdx.x & 8;
+    Pair x = add(b16 ? s[1] : s[0], other(b16 ? s[0] : s[1], 16));
+    const Pair third = add(s[2], other(s[2], 16));
+    x = add(b8 ? third : x, other(b8 ? x : third, 8));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) x = add(x, other(x, o));
+    return x;
+}
+
 // Sums of the block's s[0..2] in out[0..2], by a fixed tree.
 template <int kBlock>
 __device__ void block_sums(Pair (&s)[3], Pair* out) {
     __shared__ Pair all[3][kBlock / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-        s[j] = warp_sum(s[j]);
-        if (lane == 0) all[j][warp] = s[j];
-    }
+    const Pair mine = warp_sums(s);
+    if (lane == 0 || lane == 8 || lane == 16) all[lane == 0 ? 0 : lane == 16 ? 1 : 2][warp] = mine;
     __syncthreads();
     if (warp < 3) {
         const Pair x = warp_sum(lane < kBlock / 32 ? all[warp][lane] : Pair{0.f, 0.f});
@@ -332,8 +350,7 @@ __device__ __forceinline__ void write_stats(const PolicyArgs& a, const Pair* s) 
 }
 
 __device__ __forceinline__ Groups grid_groups(const PolicyArgs& a) {
-    return Groups(a.N, blockIdx.x * int64_t(kThreads / 32) + (threadIdx.x >> 5),
-                  int64_t(gridDim.x) * (kThreads / 32));
+    return Groups(a.N, blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32));
 }
 
 __global__ void __launch_bounds__(kThreads) policy_clear_kernel(PolicyWs* __restrict__ ws,
