@@ -24,7 +24,7 @@ constexpr int64_t kSmallTokens = 4096;    // most tokens (and sequences) of the 
 
 // Sequences of 32 tokens at a time, for a warp that walks along the tokens.
 // Its lanes hold the ends of the next 32 sequences; where they are not known
-// (the start, or past them) the warp searches, 32 probes a step.  The sequence
+// (the start, or all of them past) the warp searches, 32 probes a step.  The sequence
 // of token t is the last b with offs[b] <= t, or -1 if t lies in none; whatever
 // the offsets hold, it is in [-1, n_seqs).
 struct SeqWalk {
@@ -36,6 +36,11 @@ struct SeqWalk {
     __device__ __forceinline__ static int offset(const PolicyArgs& a, int64_t i) {
         const int64_t o = a.offs[i];
         return o < 0 ? 0 : o > 0x7fffffff ? 0x7fffffff : static_cast<int>(o);
+    }
+    __device__ __forceinline__ void load(const PolicyArgs& a, int64_t from, int lane) {
+        const int64_t i = from + 1 + lane;
+        base = static_cast<int>(from);
+        ends = i <= a.n_seqs ? offset(a, i) : 0x7fffffff;
     }
     // How many of the n_seqs + 1 offsets are <= t.
     __device__ static int64_t search(const PolicyArgs& a, int t, int lane) {
@@ -53,11 +58,10 @@ struct SeqWalk {
     __device__ __forceinline__ int at(const PolicyArgs& a, int t0, int lane) {
         const int t1 = t0 + 31, t = t0 + lane;
         if (t1 < until) return b;  // still inside
-        if (base == -2 || __shfl_sync(0xffffffffu, ends, 31) <= t1) {
-            base = static_cast<int>(search(a, t0, lane)) - 1;
-            const int64_t i = int64_t(base) + 1 + lane;
-            ends = i <= a.n_seqs ? offset(a, i) : 0x7fffffff;
-        }
+        unsigned past = ~0u;  // the start: search
+        if (base != -2) past = __ballot_sync(0xffffffffu, ends <= t0);
+        if (base == -2 || __shfl_sync(0xffffffffu, ends, 31) <= t1)
+            load(a, past == ~0u ? search(a, t0, lane) - 1 : int64_t(base) + __popc(past), lane);
         const unsigned m0 = __ballot_sync(0xffffffffu, ends <= t0);
         const unsigned m1 = __ballot_sync(0xffffffffu, ends <= t1);
         uniform = m0 == m1;
