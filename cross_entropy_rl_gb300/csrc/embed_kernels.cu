@@ -106,11 +106,11 @@ constexpr int kStaged = 4096;        // keys a CTA holds in shared memory
 // Most tokens that one CTA sorts (the sort with nothing to add up: 2048 tokens 12.0
 // us, by the cluster 13.5; 4096 tokens 15.8, by the cluster 14.0).
 constexpr int64_t kOneCta = 2048;
-// Most tokens that one launch sorts and adds (a 4096 wide BF16 gradient into FP32, and
-// the host's time of a call): 300 tokens of width 512 12.7 us, 9.5 on the host, by three
-// launches 12.2 and 13.4; 1024 tokens 16.8 and 16.3; 2048 tokens, a hot one in 0.7 of
-// them, 25.3 and 20.8.  What a call gains is the host's two launches.
-constexpr int kShortTokens = 1024;
+// Most tokens that are matched in one launch instead of sorted.  BF16 added into FP32,
+// matched and sorted: 64 x 4096 3.4 and 10.6 us, 300 x 512 5.5 and 12.2, 1024 x 1024 8.9
+// and 15.7, 1024 x 4096 16.3 and 16.2; with 0.7 of them one token 14.7 and 17.7.  2048 x
+// 256 12.3 and 17.8, but 2048 x 4096 36.8 and 21.4, and with a hot token 30.4 and 20.9.
+constexpr int kMatch = 1024;
 constexpr int kWarpStaged = kStaged / kSortWarps;
 constexpr int kRounds = 4;           // rounds of 32 keys of a warp at a time
 constexpr int kFillCtas = 256;       // CTAs in all when rows are filled beside the sort
@@ -781,6 +781,15 @@ __device__ __forceinline__ TO grad_value(float s, float old) {
     return Elem<TO>::from_f(old + (s + 0.f));
 }
 
+// Whether this block is one of `fills` that fill rows, which take turns with the others
+// from the front while there are both; `block` becomes its number among its kind.
+__device__ __forceinline__ bool fills_rows(unsigned fills, int64_t& block) {
+    const int64_t sums = gridDim.x - fills, turns = sums < fills ? sums : fills;
+    const bool fill = block < 2 * turns ? block & 1 : sums < fills;
+    block = block < 2 * turns ? block >> 1 : block - turns;
+    return fill;
+}
+
 // A warp takes a window of the sorted order, whole units of `window` entries or
 // so, and a tile of columns: C packs of E elements a lane.  Its rows lie side
 // by side in the sorted order whatever units they belong to, so R of them, and
@@ -791,95 +800,6 @@ __device__ __forceinline__ TO grad_value(float s, float old) {
 // rows in registers 4 of 4 spill nothing: 4096 x 2048 40 us, 3 of 4 44); a warp
 // per unit and tile, its rows waited for unit by unit, 209; adding to the table in L2
 // (red.v4.f32) instead of reading it 164.
-// SHORT: rows of tokens of several units, marked in each of their entries, are
-// left out.
-template <typename TI, typename TO, int E, int C, int R, bool ADD, bool SHORT>
-__device__ __forceinline__ void add_window(const TI* __restrict__ g, TO* __restrict__ dW,
-                                           const GradArgs& a, const Entry* entries, int p0, int p1,
-                                           int64_t c0) {
-    const int lane = threadIdx.x & 31;
-    bool has[C];
-#pragma unroll
-    for (int k = 0; k < C; ++k) has[k] = c0 + k * 32 * E < a.D;
-    int start = p0;  // of the unit
-    float acc[C][E];
-#pragma unroll
-    for (int k = 0; k < C; ++k)
-#pragma unroll
-        for (int j = 0; j < E; ++j) acc[k][j] = 0.f;
-    for (int b = p0; b < p1; b += 32) {
-        const Entry mine = b + lane < p1 ? entries[b + lane] : Entry{0, 0};
-        const int n = p1 - b < 32 ? p1 - b : 32;
-#pragma unroll 1
-        for (int r = 0; r < n; r += R) {
-            Pack<TI, E> x[R][C];
-            Pack<TO, E> old[ADD ? R : 1][C];
-            auto entry = [&](int q) {
-                return Entry{__shfl_sync(0xffffffffu, mine.pos, (r + q) & 31),
-                             __shfl_sync(0xffffffffu, mine.row, (r + q) & 31)};
-            };
-#pragma unroll
-            for (int q = 0; q < R; ++q) {
-                const Entry e = entry(q);
-                if (r + q < n && !(SHORT && (e.row & kTop))) {
-                    const TI* src = g + int64_t(e.pos & ~kTop) * a.ldg + c0;
-#pragma unroll
-                    for (int k = 0; k < C; ++k)
-                        if (has[k]) x[q][k].load(src + k * 32 * E);
-                    if (ADD && (e.pos & kTop) && !(e.row & kTop)) {
-                        const TO* row = dW + int64_t(e.row) * a.ldw + c0;
-#pragma unroll
-                        for (int k = 0; k < C; ++k)
-                            if (has[k]) old[ADD ? q : 0][k].load(row + k * 32 * E);
-                    }
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < R; ++q) {
-                if (r + q >= n) break;
-                const Entry e = entry(q);
-                if (SHORT && (e.row & kTop)) continue;
-#pragma unroll
-                for (int k = 0; k < C; ++k)
-#pragma unroll
-                    for (int j = 0; j < E; ++j) acc[k][j] += Elem<TI>::to_f(x[q][k].e[j]);
-                if (!(e.pos & kTop)) continue;
-                if (!(e.row & kTop)) {
-                    TO* row = dW + int64_t(e.row) * a.ldw + c0;
-#pragma unroll
-                    for (int k = 0; k < C; ++k) {
-                        Pack<TO, E> y;
-#pragma unroll
-                        for (int j = 0; j < E; ++j)
-                            y.e[j] = grad_value<TO>(
-                                a.scale * acc[k][j],
-                                ADD ? Elem<TO>::to_f(old[ADD ? q : 0][k].e[j]) : 0.f);
-                        if (has[k]) y.store(row + k * 32 * E);
-                    }
-                } else {
-                    // Full pieces have the even slot of their K positions; beside
-                    // it is the odd one, for a short last piece that starts there.
-                    const int len = b + r + q + 1 - start;
-                    float* dst =
-                        a.p.part + (int64_t(start / a.K) * 2 + (len < a.K)) * a.p.Dp + c0;
-#pragma unroll
-                    for (int k = 0; k < C; ++k) {
-                        Pack<float, E> y;
-#pragma unroll
-                        for (int j = 0; j < E; ++j) y.e[j] = acc[k][j];
-                        if (has[k]) y.store(dst + k * 32 * E);
-                    }
-                }
-                start = b + r + q + 1;
-#pragma unroll
-                for (int k = 0; k < C; ++k)
-#pragma unroll
-                    for (int j = 0; j < E; ++j) acc[k][j] = 0.f;
-            }
-        }
-    }
-}
-
 template <typename TI, typename TO, int E, int C, int R, bool ADD>
 __global__ void __launch_bounds__(32 * kGradWarps, ADD ? 3 : 4) embed_grad_kernel(
     const TI* __restrict__ g, TO* __restrict__ dW, const __grid_constant__ GradArgs a) {
@@ -888,11 +808,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, ADD ? 3 : 4) embed_grad_kerne
     launch_dependents();
     int64_t block = blockIdx.x;
     if (!ADD && a.fills) {
-        // sums and fills take turns from the front while there are both
-        const int64_t sums = gridDim.x - a.fills, turns = sums < a.fills ? sums : a.fills;
-        const bool fill = block < 2 * turns ? block & 1 : sums < a.fills;
-        block = block < 2 * turns ? block >> 1 : block - turns;
-        if (fill) {
+        if (fills_rows(a.fills, block)) {
             const int64_t v0 = block * a.fill_rows;
             const int rows = static_cast<int>(a.V - v0 < a.fill_rows ? a.V - v0 : a.fill_rows);
             fill_rows_of(reinterpret_cast<char*>(dW + v0 * a.ldw), a.ldw * int64_t(sizeof(TO)),
@@ -905,107 +821,87 @@ __global__ void __launch_bounds__(32 * kGradWarps, ADD ? 3 : 4) embed_grad_kerne
     const int64_t it = block * kGradWarps + (threadIdx.x >> 5);
     if (it < items) {
         const int64_t c0 = (it % a.tiles * C * 32 + lane) * E;
+        bool has[C];
+#pragma unroll
+        for (int k = 0; k < C; ++k) has[k] = c0 + k * 32 * E < a.D;
         const int64_t w = it / a.tiles;
-        add_window<TI, TO, E, C, R, ADD, false>(g, dW, a, a.p.entries, a.p.windows[w],
-                                                a.p.windows[w + 1], c0);
-    }
-}
-
-// Few tokens added to a table, all in one launch: each block sorts all tokens by
-// itself (entries and all in shared memory) and takes its share of the windows, and
-// of the tokens of several units, whose rows its warps share out.
-template <typename TI, typename TO, int E, int C, int R>
-__global__ void __launch_bounds__(kSortThreads) embed_short_kernel(
-    const TI* __restrict__ g, TO* __restrict__ dW, const __grid_constant__ SortArgs sort,
-    const __grid_constant__ GradArgs a) {
-    constexpr int kCols = 32 * C * E;
-    __shared__ SortHead head;
-    __shared__ int order[kShortTokens / kPiece];  // of the long tokens
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    SortArgs s = sort;  // what the sort writes takes the place of its counts
-    s.p.head = &head;
-    s.p.entries = reinterpret_cast<Entry*>(sort_smem);
-    s.p.longs = reinterpret_cast<Long*>(s.p.entries + kShortTokens);
-    s.p.windows = reinterpret_cast<int*>(s.p.longs + kShortTokens / kPiece);
-    float* sums = reinterpret_cast<float*>(sort_smem + kSortWarps * kBins * 4);  // its keys'
-    static_assert(kShortTokens * (sizeof(Entry) + sizeof(Long) / 16 + 1) <= kSortWarps * kBins * 4,
-                  "the entries fit");
-    sort_tokens<1>(s);
-    // The order of a block's list of long tokens is its own: that of their starts,
-    // no two of them in the same K positions, is every block's.
-    for (int i = tid; i < a.slots; i += kSortThreads) order[i] = -1;
-    __syncthreads();
-    const int longs = head.longs + head.huges;
-    for (int i = warp; i < longs; i += kSortWarps) {
-        const int at = i < head.longs ? i : a.slots - 1 - (i - head.longs);
-        const Long l = s.p.longs[at];
-        if (lane == 0) order[l.start / a.K] = at;
-        for (int j = lane; j < l.count; j += 32) s.p.entries[l.start + j].row |= kTop;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int n = 0;
-        for (int i = lane; i - lane < a.slots; i += 32) {
-            const int at = i < a.slots ? order[i] : -1;
-            const unsigned some = __ballot_sync(0xffffffffu, at >= 0);
-            if (at >= 0) order[n + __popc(some & ((1u << lane) - 1))] = at;
-            n += __popc(some);
-            __syncwarp();
-        }
-    }
-    const int64_t items = int64_t((head.valid + a.window - 1) / a.window) * a.tiles;
-    for (int64_t it = blockIdx.x * int64_t(kSortWarps) + warp; it < items;
-         it += int64_t(gridDim.x) * kSortWarps) {
-        const int64_t w = it / a.tiles;
-        add_window<TI, TO, E, C, R, true, true>(g, dW, a, s.p.entries, s.p.windows[w],
-                                               s.p.windows[w + 1],
-                                               (it % a.tiles * C * 32 + lane) * E);
-    }
-    __syncthreads();  // the order is there
-    for (int it = blockIdx.x; it < longs * a.tiles; it += gridDim.x) {
-        const Long l = s.p.longs[order[it / a.tiles]];
-        const int64_t c1 = it % a.tiles * int64_t(kCols);
-        const int per = (l.count + kSortWarps - 1) / kSortWarps;
-        const int p0 = warp * per, p1 = min(p0 + per, l.count);
+        const int p0 = a.p.windows[w], p1 = a.p.windows[w + 1];
+        int start = p0;  // of the unit
         float acc[C][E];
 #pragma unroll
         for (int k = 0; k < C; ++k)
 #pragma unroll
             for (int j = 0; j < E; ++j) acc[k][j] = 0.f;
-        for (int p = p0; p < p1; p += 2 * R) {
-            Pack<TI, E> x[2 * R][C];
+        for (int b = p0; b < p1; b += 32) {
+            const Entry mine = b + lane < p1 ? a.p.entries[b + lane] : Entry{0, 0};
+            const int n = p1 - b < 32 ? p1 - b : 32;
+#pragma unroll 1
+            for (int r = 0; r < n; r += R) {
+                Pack<TI, E> x[R][C];
+                Pack<TO, E> old[ADD ? R : 1][C];
+                auto entry = [&](int q) {
+                    return Entry{__shfl_sync(0xffffffffu, mine.pos, (r + q) & 31),
+                                 __shfl_sync(0xffffffffu, mine.row, (r + q) & 31)};
+                };
 #pragma unroll
-            for (int q = 0; q < 2 * R; ++q) {
-                if (p + q >= p1) break;
-                const TI* src = g + int64_t(s.p.entries[l.start + p + q].pos & ~kTop) * a.ldg + c1;
+                for (int q = 0; q < R; ++q) {
+                    const Entry e = entry(q);
+                    if (r + q < n) {
+                        const TI* src = g + int64_t(e.pos & ~kTop) * a.ldg + c0;
 #pragma unroll
-                for (int k = 0; k < C; ++k) {
-                    const int c = (k * 32 + lane) * E;
-                    if (c1 + c < a.D) x[q][k].load(src + c);
+                        for (int k = 0; k < C; ++k)
+                            if (has[k]) x[q][k].load(src + k * 32 * E);
+                        if (ADD && (e.pos & kTop) && !(e.row & kTop)) {
+                            const TO* row = dW + int64_t(e.row) * a.ldw + c0;
+#pragma unroll
+                            for (int k = 0; k < C; ++k)
+                                if (has[k]) old[ADD ? q : 0][k].load(row + k * 32 * E);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    if (r + q >= n) break;
+#pragma unroll
+                    for (int k = 0; k < C; ++k)
+#pragma unroll
+                        for (int j = 0; j < E; ++j) acc[k][j] += Elem<TI>::to_f(x[q][k].e[j]);
+                    const Entry e = entry(q);
+                    if (!(e.pos & kTop)) continue;
+                    if (!(e.row & kTop)) {
+                        TO* row = dW + int64_t(e.row) * a.ldw + c0;
+#pragma unroll
+                        for (int k = 0; k < C; ++k) {
+                            Pack<TO, E> y;
+#pragma unroll
+                            for (int j = 0; j < E; ++j)
+                                y.e[j] = grad_value<TO>(
+                                    a.scale * acc[k][j],
+                                    ADD ? Elem<TO>::to_f(old[ADD ? q : 0][k].e[j]) : 0.f);
+                            if (has[k]) y.store(row + k * 32 * E);
+                        }
+                    } else {
+                        // Full pieces have the even slot of their K positions; beside
+                        // it is the odd one, for a short last piece that starts there.
+                        const int len = b + r + q + 1 - start;
+                        float* dst =
+                            a.p.part + (int64_t(start / a.K) * 2 + (len < a.K)) * a.p.Dp + c0;
+#pragma unroll
+                        for (int k = 0; k < C; ++k) {
+                            Pack<float, E> y;
+#pragma unroll
+                            for (int j = 0; j < E; ++j) y.e[j] = acc[k][j];
+                            if (has[k]) y.store(dst + k * 32 * E);
+                        }
+                    }
+                    start = b + r + q + 1;
+#pragma unroll
+                    for (int k = 0; k < C; ++k)
+#pragma unroll
+                        for (int j = 0; j < E; ++j) acc[k][j] = 0.f;
                 }
             }
-#pragma unroll
-            for (int q = 0; q < 2 * R; ++q) {
-                if (p + q >= p1) break;
-#pragma unroll
-                for (int k = 0; k < C; ++k)
-#pragma unroll
-                    for (int j = 0; j < E; ++j) acc[k][j] += Elem<TI>::to_f(x[q][k].e[j]);
-            }
         }
-#pragma unroll
-        for (int k = 0; k < C; ++k)
-#pragma unroll
-            for (int j = 0; j < E; ++j) sums[warp * kCols + (k * 32 + lane) * E + j] = acc[k][j];
-        __syncthreads();
-        if (tid < kCols && c1 + tid < a.D) {
-            const int used = (l.count + per - 1) / per;
-            float f = sums[tid];
-            for (int w = 1; w < used; ++w) f += sums[w * kCols + tid];
-            TO* p = dW + int64_t(l.row) * a.ldw + c1 + tid;
-            *p = grad_value<TO>(a.scale * f, Elem<TO>::to_f(*p));
-        }
-        __syncthreads();
     }
 }
 
@@ -1078,6 +974,210 @@ __global__ void __launch_bounds__(32 * kGradWarps) embed_join_kernel(
     }
 }
 
+// Few tokens, in one launch and without a sort: a warp takes a position and a tile of
+// columns, looks in all tokens (in shared memory) for those of the same row and, if
+// none is ahead of its own, adds up their rows in order.  Rows of a token of more than
+// kPiece are shared out, in order, over the block's warps once they are done.  Bound
+// by latency: tokens, rows and the table's rows are three trips to memory (a launch
+// alone 2.2 us).  A warp that looked once for several tiles of columns was faster
+// without hot tokens (1024 x 4096 14.4 us) and slower with them (20.3).
+struct MatchArgs {
+    const int64_t* tokens;
+    int N, tiles;
+    int64_t V, v0, ldg, D, ldw, row_bytes;
+    float scale;
+    int fill_rows;   // as in GradArgs, any number
+    unsigned fills;
+};
+constexpr int kMatchThreads = 512;
+constexpr int kMatchWarps = kMatchThreads / 32;
+constexpr int kMatchInFlight = 4;  // rows of a warp
+constexpr int kMatchRows = 4096;  // most rows that a block fills
+static_assert(kMatch % 128 == 0 && kMatch / kMatchWarps >= kPiece, "a warp's share of a token");
+
+// The positions of row v among the first `end` of rows, 128 at a time: take(p, k) by
+// the lane of the k-th position p; more(n, p) with their number so far and the first
+// of them says whether to go on.  Returns their number.
+template <typename T, typename M>
+__device__ __forceinline__ int match(const int* rows, int end, int v, const T& take, const M& more) {
+    const int lane = threadIdx.x & 31;
+    const unsigned under = (1u << lane) - 1;
+    int n = 0;
+#pragma unroll 2
+    for (int c = 0; c < end; c += 128) {
+        const int4 r = *reinterpret_cast<const int4*>(rows + c + lane * 4);
+        const bool is[4] = {r.x == v, r.y == v, r.z == v, r.w == v};
+        if (!__any_sync(0xffffffffu, is[0] || is[1] || is[2] || is[3])) continue;
+        int k = n, all = 0;
+        unsigned any = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const unsigned m = __ballot_sync(0xffffffffu, is[j]);
+            k += __popc(m & under);
+            all += __popc(m);
+            any |= m;
+        }
+        const int first = is[0] ? 0 : is[1] ? 1 : is[2] ? 2 : 3, low = __ffs(any) - 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (is[j]) take(c + lane * 4 + j, k++);
+        n += all;
+        if (!more(n, c + low * 4 + __shfl_sync(0xffffffffu, first, low))) break;
+    }
+    return n;
+}
+
+template <typename TI, typename TO, int E, int C, int R, bool ADD>
+__global__ void __launch_bounds__(kMatchThreads, 2) embed_match_kernel(
+    const TI* __restrict__ g, TO* __restrict__ dW, const __grid_constant__ MatchArgs a) {
+    constexpr int kCols = 32 * C * E;
+    __shared__ __align__(16) int rows[kMatch];
+    __shared__ int lists[kMatchWarps][kMatch / kMatchWarps];
+    __shared__ float sums[kMatchWarps * kCols];
+    __shared__ int longs[kMatchWarps];  // the rows of a warp's token, if that has more than kPiece
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t block = blockIdx.x;
+    if (!ADD && fills_rows(a.fills, block)) {
+        unsigned* marks = reinterpret_cast<unsigned*>(rows);
+        static_assert(kMatchRows <= kMatch * 32, "the marks fit");
+        const int64_t r0 = block * a.fill_rows;
+        const int n = static_cast<int>(a.V - r0 < a.fill_rows ? a.V - r0 : a.fill_rows);
+        for (int i = tid; i < (n + 31) / 32; i += kMatchThreads) marks[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < a.N; i += kMatchThreads) {
+            const int64_t t = a.tokens[i], r = t - a.v0 - r0;
+            if (t >= a.v0 && r >= 0 && r < n) atomicOr(marks + (r >> 5), 1u << (r & 31));
+        }
+        __syncthreads();
+        const int step = rows_together(a.row_bytes, 8192), pitch = sizeof(TO);
+        for (int v = warp * step; v < n; v += kMatchWarps * step)
+            fill_rows_of(reinterpret_cast<char*>(dW + (r0 + v) * a.ldw), a.ldw * pitch, a.row_bytes,
+                         n - v < step ? n - v : step, marks[v >> 5] >> (v & 31), lane, 32);
+        return;
+    }
+    const int end = (a.N + 127) / 128 * 128;
+    for (int i = tid; i < end; i += kMatchThreads) {
+        int row = -1;
+        if (i < a.N) {
+            const int64_t y = a.tokens[i], v = y - a.v0;
+            if (y >= a.v0 && v < a.V) row = static_cast<int>(v);
+        }
+        rows[i] = row;
+    }
+    __syncthreads();
+    // neighbouring blocks take neighbouring tiles, so that a token's are spread
+    const int blocks = gridDim.x - (ADD ? 0 : a.fills);
+    auto item = [&](int w) { return w * blocks + static_cast<int>(block); };
+    auto token_of = [&](int w) { return item(w) / a.tiles; };
+    auto column = [&](int w) { return item(w) % a.tiles * int64_t(kCols); };
+    float acc[C][E];
+    auto clear = [&]() {
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+#pragma unroll
+            for (int j = 0; j < E; ++j) acc[k][j] = 0.f;
+    };
+    const int* mine = lists[warp];
+    auto load_rows = [&](auto& x, int p, int n, int64_t c0) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            if (p + q >= n) break;
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                if (c0 + (k * 32 + lane) * E < a.D)
+                    x[q][k].load(g + mine[p + q] * a.ldg + c0 + (k * 32 + lane) * E);
+        }
+    };
+    auto add_rows = [&](const auto& x, int p, int n) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            if (p + q >= n) break;
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+#pragma unroll
+                for (int j = 0; j < E; ++j) acc[k][j] += Elem<TI>::to_f(x[q][k].e[j]);
+        }
+    };
+
+    const int i = token_of(warp);
+    const int v = i < a.N ? rows[i] : -1;
+    int n = 0;
+    if (v >= 0) {
+        bool first = true;
+        n = match(
+            rows, end, v,
+            [&](int p, int k) {
+                if (k < kPiece) lists[warp][k] = p;
+            },
+            [&](int so_far, int p) {
+                if (n == 0 && p != i) first = false;
+                n = so_far;
+                return first;
+            });
+        if (!first) n = 0;
+        __syncwarp();
+    }
+    if (lane == 0) longs[warp] = n > kPiece ? n : 0;
+    if (n > 0 && n <= kPiece) {
+        const int64_t c0 = column(warp);
+        TO* row = dW + int64_t(v) * a.ldw + c0;
+        Pack<TO, E> old[C];
+        if (ADD) {
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                if (c0 + (k * 32 + lane) * E < a.D) old[k].load(row + (k * 32 + lane) * E);
+        }
+        clear();
+        for (int p = 0; p < n; p += R) {
+            Pack<TI, E> x[R][C];
+            load_rows(x, p, n, c0);
+            add_rows(x, p, n);
+        }
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            Pack<TO, E> y;
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                y.e[j] = grad_value<TO>(a.scale * acc[k][j], ADD ? Elem<TO>::to_f(old[k].e[j]) : 0.f);
+            if (c0 + (k * 32 + lane) * E < a.D) y.store(row + (k * 32 + lane) * E);
+        }
+    }
+    __syncthreads();
+    for (int w = 0; w < kMatchWarps; ++w) {
+        const int all = longs[w];
+        if (all == 0) continue;
+        const int row = rows[token_of(w)], per = (all + kMatchWarps - 1) / kMatchWarps;
+        const int64_t c0 = column(w);
+        const int p0 = warp * per, p1 = min(p0 + per, all);
+        match(
+            rows, end, row,
+            [&](int p, int k) {
+                if (k >= p0 && k < p1) lists[warp][k - p0] = p;
+            },
+            [&](int so_far, int) { return so_far < p1; });
+        __syncwarp();
+        clear();
+        for (int p = 0; p < p1 - p0; p += R) {
+            Pack<TI, E> x[R][C];
+            load_rows(x, p, p1 - p0, c0);
+            add_rows(x, p, p1 - p0);
+        }
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+#pragma unroll
+            for (int j = 0; j < E; ++j) sums[warp * kCols + (k * 32 + lane) * E + j] = acc[k][j];
+        __syncthreads();
+        if (tid < kCols && c0 + tid < a.D) {
+            const int used = (all + per - 1) / per;
+            float f = sums[tid];
+            for (int u = 1; u < used; ++u) f += sums[u * kCols + tid];
+            TO* p = dW + int64_t(row) * a.ldw + c0 + tid;
+            *p = grad_value<TO>(a.scale * f, ADD ? Elem<TO>::to_f(*p) : 0.f);
+        }
+        __syncthreads();
+    }
+}
+
 // Whole 16-byte packs of rows that start on 16-byte boundaries.
 bool grad_vec(const EmbedArgs& a) {
     return a.D % (a.dtype == LL_F32 ? 4 : 8) == 0 &&
@@ -1085,23 +1185,9 @@ bool grad_vec(const EmbedArgs& a) {
            rows16(a.table, a.ld_table, a.table_dtype == LL_F32 ? 4 : 2);
 }
 
-bool one_launch(const EmbedArgs& e, int accumulate) { return accumulate && e.N <= kShortTokens; }
-
-// Lets a kernel have `bytes` of dynamic shared memory, once on a device.
-template <typename F>
-cudaError_t give_smem(F* kernel, int bytes, const DevInfo& dev, std::atomic<uint64_t>& ready) {
-    const uint64_t bit = uint64_t(1) << dev.device;
-    if (ready.load() & bit) return cudaSuccess;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) ready.fetch_or(bit);
-    return e;
-}
-
 template <typename TI, typename TO>
-cudaError_t grad_typed(const EmbedArgs& e, bool vec, int accumulate, GradArgs a,
-                       const SortArgs& sort, const DevInfo& dev, cudaStream_t s) {
-    const int num_sms = dev.num_sms;
+cudaError_t grad_typed(const EmbedArgs& e, bool vec, int accumulate, GradArgs a, int num_sms,
+                       cudaStream_t s) {
     constexpr int E = 16 / sizeof(TI), C1 = 4;
     const int64_t cols = vec ? 32 * E : 32 * C1;
     a.tiles = static_cast<int>((a.D + cols - 1) / cols);
@@ -1119,19 +1205,25 @@ cudaError_t grad_typed(const EmbedArgs& e, bool vec, int accumulate, GradArgs a,
     const int64_t long_items = e.N / a.K * ((a.D + 127) / 128);
     const int64_t full = int64_t(num_sms) * 8;
     const unsigned join_blocks = static_cast<unsigned>(full < long_items ? full : long_items);
-    if (one_launch(e, accumulate)) {
-        const int64_t blocks_of = (items + kSortWarps - 1) / kSortWarps;
-        const int64_t most = blocks_of < num_sms ? blocks_of : num_sms;
-        auto run = [&](auto* kernel, std::atomic<uint64_t>& ready) {
-            const cudaError_t err = give_smem(kernel, kSortSmem, dev, ready);
-            if (err != cudaSuccess) return err;
+    if (e.N <= kMatch) {
+        const int64_t all = (e.N * a.tiles + kMatchWarps - 1) / kMatchWarps;
+        MatchArgs m{e.tokens, static_cast<int>(e.N), a.tiles, e.V, e.v0, a.ldg, a.D, a.ldw,
+                    a.row_bytes, a.scale, 1, 0};
+        while (m.fill_rows * 2 * a.row_bytes <= kFillBytes && m.fill_rows < kMatchRows)
+            m.fill_rows *= 2;
+        if (!accumulate) m.fills = static_cast<unsigned>((e.V + m.fill_rows - 1) / m.fill_rows);
+        if (all * kMatchWarps + m.fills > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        auto run = [&](auto* kernel) {
             note_launches(1);
-            kernel<<<static_cast<unsigned>(most), kSortThreads, kSortSmem, s>>>(g, dW, sort, a);
+            kernel<<<static_cast<unsigned>(all + m.fills), kMatchThreads, 0, s>>>(g, dW, m);
             return cudaGetLastError();
         };
-        static std::atomic<uint64_t> ready[2];
-        return vec ? run(embed_short_kernel<TI, TO, E, 1, kGradRows>, ready[0])
-                   : run(embed_short_kernel<TI, TO, 1, C1, kGradRows>, ready[1]);
+        constexpr int R = kMatchInFlight;
+        if (vec)
+            return accumulate ? run(embed_match_kernel<TI, TO, E, 1, R, true>)
+                              : run(embed_match_kernel<TI, TO, E, 1, R, false>);
+        return accumulate ? run(embed_match_kernel<TI, TO, 1, C1, R, true>)
+                          : run(embed_match_kernel<TI, TO, 1, C1, R, false>);
     }
     auto run = [&](auto* sums, auto* join) {
         note_launches(join_blocks ? 2 : 1);
@@ -1210,6 +1302,18 @@ static int bits_of(int64_t V) {
     return b;
 }
 
+// Lets a kernel have `bytes` of dynamic shared memory, once on a device.
+template <typename F>
+static cudaError_t give_smem(F* kernel, int bytes, const DevInfo& dev,
+                             std::atomic<uint64_t>& ready) {
+    const uint64_t bit = uint64_t(1) << dev.device;
+    if (ready.load() & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit);
+    return e;
+}
+
 static cudaError_t launch_big_sort(const SortArgs& a, const DevInfo& dev, cudaStream_t s) {
     static std::atomic<uint64_t> ready;
     cudaError_t e = give_smem(embed_count_kernel, kCountSmem, dev, ready);
@@ -1240,7 +1344,9 @@ static cudaError_t launch_big_sort(const SortArgs& a, const DevInfo& dev, cudaSt
     return launch_after(embed_entries_kernel, blocks, kSortThreads, s, 0, a, b.src);
 }
 
-static SortArgs sort_args(const EmbedArgs& e, int accumulate, void* ws) {
+cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, const DevInfo& dev,
+                              cudaStream_t s) {
+    if (e.N <= kMatch) return cudaSuccess;  // not sorted
     size_t bytes;
     SortArgs a;
     a.tokens = e.tokens;
@@ -1259,13 +1365,6 @@ static SortArgs sort_args(const EmbedArgs& e, int accumulate, void* ws) {
     a.pitch = e.ld_table * es;
     a.now = 0.f;
     a.mark = e.N > kStaged * kSortCtas && !accumulate;
-    return a;
-}
-
-cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, const DevInfo& dev,
-                              cudaStream_t s) {
-    if (one_launch(e, accumulate)) return cudaSuccess;  // in the launch of the sums
-    SortArgs a = sort_args(e, accumulate, ws);
     if (e.N > kStaged * kSortCtas) return launch_big_sort(a, dev, s);
     // The sort takes about 10 us and 0.3 us per thousand tokens.
     const double beside = 48e6 + 1600.0 * static_cast<double>(e.N);
@@ -1294,6 +1393,7 @@ cudaError_t launch_embed_sort(const EmbedArgs& e, int accumulate, void* ws, cons
 
 cudaError_t launch_embed_bwd(const EmbedArgs& e, int accumulate, void* ws, const DevInfo& dev,
                              cudaStream_t s) {
+    const int num_sms = dev.num_sms;
     size_t bytes;
     const bool vec = grad_vec(e);
     GradArgs a;
@@ -1306,18 +1406,17 @@ cudaError_t launch_embed_bwd(const EmbedArgs& e, int accumulate, void* ws, const
     a.window = window_rows(e.N);
     a.slots = static_cast<int>((e.N + a.K - 1) / a.K);
     a.p = grad_layout(e.N, e.D, e.V, ws, &bytes);
-    const SortArgs sort = sort_args(e, accumulate, ws);
     switch (e.dtype * 3 + e.table_dtype) {
         case LL_F32 * 3 + LL_F32:
-            return grad_typed<float, float>(e, vec, accumulate, a, sort, dev, s);
+            return grad_typed<float, float>(e, vec, accumulate, a, num_sms, s);
         case LL_F16 * 3 + LL_F16:
-            return grad_typed<__half, __half>(e, vec, accumulate, a, sort, dev, s);
+            return grad_typed<__half, __half>(e, vec, accumulate, a, num_sms, s);
         case LL_F16 * 3 + LL_F32:
-            return grad_typed<__half, float>(e, vec, accumulate, a, sort, dev, s);
+            return grad_typed<__half, float>(e, vec, accumulate, a, num_sms, s);
         case LL_BF16 * 3 + LL_BF16:
-            return grad_typed<__nv_bfloat16, __nv_bfloat16>(e, vec, accumulate, a, sort, dev, s);
+            return grad_typed<__nv_bfloat16, __nv_bfloat16>(e, vec, accumulate, a, num_sms, s);
         default:
-            return grad_typed<__nv_bfloat16, float>(e, vec, accumulate, a, sort, dev, s);
+            return grad_typed<__nv_bfloat16, float>(e, vec, accumulate, a, num_sms, s);
     }
 }
 
