@@ -88,7 +88,8 @@ bool rows16(const void* p, int64_t ld, size_t es) {
 }
 
 // ----------------------------------------------------------------- gradient
-// Three launches.  The first sorts the tokens (one cluster), the second adds up
+// Few tokens are matched in one launch (embed_match_kernel).  Others take three
+// launches.  The first sorts the tokens (one cluster), the second adds up
 // the rows of grad_out in the sorted order, the third finishes long tokens.
 //
 // A unit is at most K sorted positions of one token: a token's occurrences are
@@ -384,7 +385,7 @@ __device__ __forceinline__ void write_head(const SortArgs& a, int64_t M) {
 // there, and a key goes to its place in the other buffer of the CTA whose run that
 // is.  The loops are kept short: the sort is some ten thousand cycles long and its
 // instructions are fetched cold (eight rounds unrolled, counting 300 tokens took
-// 3.2k cycles instead of 0.9k).  300 / 4096 / 32768 tokens: 6 / 11 / 20 us.
+// 3.2k cycles instead of 0.9k).  4096 / 32768 tokens: 11 / 20 us.
 template <int CTAS>
 __device__ void sort_tokens(const SortArgs& a) {
     int* hist = reinterpret_cast<int*>(sort_smem);  // [kSortWarps][bins]
