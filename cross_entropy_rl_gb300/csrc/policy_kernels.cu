@@ -8,7 +8,9 @@
 //
 // ~20 FP32 operations and at most 21 bytes per token: a batch of a million
 // tokens is 21 MB, so the launches and the two dependent passes (the weights
-// need the counts) are what costs.
+// need the counts) are what costs, and instructions: 250 per 32 tokens of the
+// second pass, whose issue slots are 56% used.  4096 / a million tokens 5.6 / 14.5 us,
+// a million in 700 sequences 21.5.
 #include <math.h>
 
 #include "ll_device.cuh"
