@@ -331,3 +331,23 @@ def test_graph_of_few_tokens_added(lib):
     graph.replay()
     torch.cuda.synchronize()
     assert bits_equal(dA, lib.embed_backward(g, y, V, out=torch.zeros_like(dA), accumulate=True))
+
+
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("N,D,V,hot,pad,shift", [
+    (1, 3, 70000, 0, 5, 1), (100, 1, 500000, 0, 0, 0), (777, 72, 20000, 0.1, 8, 0),
+    (1023, 1031, 300, 0.3, 3, 1), (1024, 2048, 900, 0, 0, 0), (1024, 136, 1, 0, 0, 0)])
+def test_few_tokens_into_a_table_of_their_own(lib, dt, out, N, D, V, hot, pad, shift):
+    """Few tokens, every row of the table written, and nothing beside the rows."""
+    g = table(N, D, dt, 81)
+    y = ids(N, V, 82, hot, invalid=0.05)
+    dW = table(V, D, out, 83, pad, shift)
+    beside = dW.as_strided((V, dW.stride(0)), (dW.stride(0), 1))[:-1, D:]
+    was = beside.clone()
+    lib.embed_backward(g, torch.from_numpy(y).cuda(), V, scale=-0.5, out=dW)
+    r, M, c = reference(g, y, V, -0.5, None)
+    check_grad(dW, r, M, c, out)
+    none = torch.from_numpy(c == 0).cuda()
+    if none.any():
+        assert_pos_zero("rows of no token", dW[none])
+    assert bits_equal(beside.contiguous(), was)

@@ -262,3 +262,27 @@ def test_runs_streams_and_graphs(lib):
     graph.replay()
     d = lib.policy_loss(logp, old, adv, **kw)
     assert bits_equal(d[0], out[0]) and bits_equal(d[1], out[1]) and not bits_equal(a[1], out[1])
+
+
+@pytest.mark.parametrize("kind", ["one", "few", "thousands", "short", "clumps", "partial"])
+@pytest.mark.parametrize("N", [5003, 1000003])
+def test_every_token_has_its_sequence(lib, kind, N):
+    """Weights alone: with a ratio of 1 and an advantage of -1 a token's gradient is
+    1 / (tokens of its sequence x sequences), an FP32 quotient of a rounded one."""
+    rng = np.random.default_rng(N)
+    cuts = {"one": 0, "few": N // 1500, "thousands": N // 60, "short": N // 2, "clumps": N // 400,
+            "partial": 50}[kind]
+    at = np.sort(rng.integers(0, N + 1, cuts))
+    if kind == "clumps":  # a hundred empty sequences at every cut
+        at = np.repeat(at, 101)
+    offs = np.concatenate([[0], at, [N]]) if kind != "partial" else at
+    mask = rng.random(N) < 0.7
+    seq = np.searchsorted(offs, np.arange(N), side="right") - 1
+    ok = mask & (seq >= 0) & (seq < len(offs) - 1)
+    count = np.bincount(seq[ok], minlength=len(offs) - 1)
+    want = np.where(ok, 1.0 / (np.maximum(count[np.clip(seq, 0, len(offs) - 2)], 1) *
+                               float((count > 0).sum())), 0.0)
+    x = torch.zeros(N, device="cuda")
+    stats, grad = run(lib, x, x, x - 1, mask=mask, offs=offs.astype(np.int64))
+    assert (np.abs(host64(grad) - want) <= 2.0 ** -23 * 1.001 * want).all()
+    assert abs(float(stats[0]) - 1) <= 2.0 ** -23 and float(stats[3]) == 0
