@@ -88,10 +88,10 @@ __device__ __forceinline__ void each_part(const GradList<N>& L, int64_t c0, int6
     }
 }
 
-// A thread's sum of squares: FP32 sums of at most kUnroll packs, added as a pair
-// while their largest element lies in [2^-50, 2^55], where neither the squares
-// nor their sums leave the FP32 range nor lose what matters; others are squared
-// in 64 bits.
+// A thread's sum of squares: FP32 sums of at most 32 elements, added as a pair
+// while their largest lies in [2^-50, 2^38], where the squares lose nothing that
+// matters and no sum of a block leaves the FP32 range: the 2^57 elements that a
+// launch accepts are 2^49 a block, of 2^76 each.  Others are squared in 64 bits.
 struct Squares {
     Pair sum = {0.f, 0.f};
     double wide = 0;
@@ -105,7 +105,7 @@ struct Squares {
             s = fmaf(x[i], x[i], s);
             big = fmaxf(big, fabsf(x[i]));  // a NaN is in s
         }
-        if (big == 0.f || (big >= 0x1p-50f && big <= 0x1p55f)) {
+        if (big == 0.f || (big >= 0x1p-50f && big <= 0x1p38f)) {
             sum = add(sum, Pair{s, 0.f});
         } else {
             used_wide = true;
@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) grad_squares_kernel(
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-// The root of the sum of the blocks' sums.
+// The root of the sum of the blocks' sums: in pairs, as a block's are, while they
+// lie in [2^-90, 2^90], of which FP32 holds almost 2^38 (2^28 launches').
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* __restrict__ part,
                                                              int64_t parts,
                                                              float* __restrict__ norm) {
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* __res
     Squares q;
     for (int64_t i = threadIdx.x; i < parts; i += kThreads) {
         const double s = part[i];
-        if (s == 0.0 || (s >= 0x1p-90 && s <= 0x1p110)) {
+        if (s == 0.0 || (s >= 0x1p-90 && s <= 0x1p90)) {
             q.sum = add(q.sum, pair_of(s));
         } else {
             q.wide += s;

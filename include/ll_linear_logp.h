@@ -524,9 +524,10 @@ size_t ll_grad_norm_workspace_size(int64_t count);
 /*
  * Norm of all gradients as one vector: norm[0] = sqrt(sum of squares over
  * every element of every tensor), FP32 on the device.  The squares are summed
- * in FP32 over short runs and in 64 bits beyond; runs whose largest element
- * is outside [2^-50, 2^55] in magnitude are squared in 64 bits, so nothing
- * overflows or vanishes on the way.  A NaN or an infinity gives NaN or
+ * in FP32 over runs of at most 32 elements and as pairs of FP32 values (about 48
+ * bits) beyond; runs whose largest element is outside [2^-50, 2^38] in magnitude
+ * are squared and summed in 64 bits, so nothing overflows or vanishes on the way,
+ * however many elements there are.  A NaN or an infinity gives NaN or
  * infinity.  The same list gives the same bits.  No tensors: norm = 0.
  */
 int ll_grad_norm(const ll_tensor* tensors, int64_t count, float* norm, void* workspace,
