@@ -400,11 +400,13 @@ cudaError_t launch_grad_norm(const ll_tensor* t, int64_t count, float* norm, voi
 
 cudaError_t launch_grad_clip(const ll_tensor* t, int64_t count, float max_norm, bool compute,
                              float* norm, void* ws, int num_sms, cudaStream_t s) {
-    if (compute && is_small(t, count)) return launch_small(t, count, max_norm, norm, s);
+    const bool clip = max_norm < INFINITY;
+    if (compute && clip && is_small(t, count)) return launch_small(t, count, max_norm, norm, s);
     if (compute) {
         const cudaError_t e = launch_grad_norm(t, count, norm, ws, num_sms, s);
         if (e != cudaSuccess) return e;
     }
+    if (!clip) return cudaSuccess;
     return count <= kFewTensors ? clip_by<kFewTensors>(t, count, max_norm, norm, num_sms, s)
                                 : clip_by<kMaxTensors>(t, count, max_norm, norm, num_sms, s);
 }

@@ -540,8 +540,8 @@ int ll_grad_norm(const ll_tensor* tensors, int64_t count, float* norm, void* wor
  *   norm_given = 0: norm[0] is computed as in ll_grad_norm and written.
  *   norm_given = 1: norm[0] (device) is read: for a norm over more than this
  *     list (gradients sharded over ranks).  No workspace.
- * max_norm > 0 (infinity: no clipping).  No two tensors may overlap
- * (LL_ERR_INVALID_ARG).
+ * max_norm > 0; infinity: no clipping, no gradient is written whatever the norm.
+ * No two tensors may overlap (LL_ERR_INVALID_ARG).
  */
 int ll_clip_grads(const ll_tensor* tensors, int64_t count, float max_norm, int norm_given,
                   float* norm, void* workspace, size_t ws_bytes, void* stream);

@@ -11,6 +11,8 @@ import math
 import pytest
 import torch
 
+from gpu_util import bits_equal
+
 pytestmark = pytest.mark.gpu
 
 E = 2.0 ** -24
@@ -55,3 +57,16 @@ def test_norm_of_random_elements(lib, sizes, scale):
     ts = [torch.randn(s, device="cuda", generator=g) * scale for s in sizes]
     want = math.sqrt(math.fsum(float(t.double().square().sum()) for t in ts))
     assert abs(float(lib.grad_norm(ts)) - want) <= NORM * want
+
+
+@pytest.mark.parametrize("n", [2000, 700001])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("given", [False, True])
+def test_an_infinite_bound_writes_nothing(lib, n, bad, given):
+    """max_norm = infinity: no clipping, whatever the norm."""
+    ts = [torch.randn(n, device="cuda"), torch.randn(33, device="cuda").bfloat16()]
+    ts[0][n // 2] = bad
+    keep = [t.clone() for t in ts]
+    norm = lib.clip_grads(ts, float("inf"), norm=lib.grad_norm(ts) if given else None)
+    assert math.isnan(bad) and math.isnan(float(norm)) or float(norm) == float("inf")
+    assert all(bits_equal(a, b) for a, b in zip(ts, keep))
