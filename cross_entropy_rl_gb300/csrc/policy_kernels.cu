@@ -349,7 +349,8 @@ __device__ __forceinline__ Pair load_pair(const PolicyWs* ws, int i) {
 
 __device__ __forceinline__ void write_stats(const PolicyArgs& a, const Pair* s) {
     const double p = double(s[0].hi) + s[0].lo, k = double(s[1].hi) + s[1].lo;
-    a.stats[0] = static_cast<float>(p + a.beta_d * k);
+    // without a weight the divergence is watched only: 0 times an infinite one is NaN
+    a.stats[0] = static_cast<float>(a.beta != 0.f ? p + a.beta_d * k : p);
     a.stats[1] = s[0].hi;
     a.stats[2] = s[1].hi;
     a.stats[3] = s[2].hi;

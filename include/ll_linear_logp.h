@@ -482,7 +482,7 @@ size_t ll_policy_workspace_size(int64_t N, int64_t n_seqs);
  *             (A < 0 and delta < log(1 - clip_low))
  *   p = -A * (clipped ? the bound : r)     (-min(r A, clamp(r) A); 0 if A == 0)
  *   k = exp(d) - d - 1                     (0 without ref_logp)
- *   loss = sum_t w_t (p_t + kl_coef k_t)
+ *   loss = sum_t w_t (p_t + kl_coef k_t)   (without k_t when kl_coef == 0)
  *   grad_logp_t = w_t ((clipped ? 0 : -A r) - kl_coef (exp(d) - 1))
  * Weights: w_t = 0 where mask_t == 0, else
  *   seq_offsets == NULL: 1 / denominator (default: the number of unmasked tokens)
