@@ -647,12 +647,23 @@ def _stream_of(device, stream):
     return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
-def _new(shape, dtype, device, stream):
-    """A new tensor for a call.  On a stream of the caller's the allocator may
-    not hand it out again before that stream is done with it."""
-    t = _torch().empty(shape, dtype=dtype, device=device)
-    if stream is not None and t.is_cuda:
-        t.record_stream(stream)
+def _new(shape, dtype, device, stream, scratch=False):
+    """A new tensor for a call on the current stream, or on `stream`.
+
+    The allocator hands a block that was freed on a stream to that stream alone:
+    work queued there may still use it.  So what `stream` writes comes from its
+    own memory.  The caller may use it on the current stream and then drop it, so
+    the allocator also waits for that one, unless it is scratch of the call."""
+    torch = _torch()
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    if stream == here:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(here)
     return t
 
 
@@ -660,7 +671,7 @@ def _scratch(workspace, nbytes, device, stream):
     """The given workspace, checked, or a new one."""
     torch = _torch()
     if workspace is None:
-        return _new((max(nbytes, 256),), torch.uint8, device, stream)
+        return _new((max(nbytes, 256),), torch.uint8, device, stream, scratch=True)
     _vector(workspace, "workspace", workspace.numel(), torch.uint8, device)
     return workspace
 
