@@ -247,12 +247,32 @@ def _check_linear(hidden, weight, bias, targets):
     return N, D, V, dev
 
 
-def _workspace(nbytes, device):
+def _new(shape, dtype, device, stream, scratch=False):
+    """A new tensor for a call on the current stream, or on `stream`.
+
+    The allocator hands a block that was freed on a stream to that stream alone:
+    work queued there may still use it.  So what `stream` writes comes from its
+    own memory.  The caller may use it on the current stream and then drop it, so
+    the allocator also waits for that one, unless it is scratch of the call."""
     torch = _torch()
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    if stream == here:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(here)
+    return t
 
 
-def _grad_outputs(out, need_dh, need_dw, need_db, N, D, V, op_dtype, dh_dtype, dw_dtype, dev):
+def _workspace(nbytes, device, stream):
+    return _new((max(int(nbytes), 256),), _torch().uint8, device, stream, scratch=True)
+
+
+def _grad_outputs(out, need_dh, need_dw, need_db, N, D, V, op_dtype, dh_dtype, dw_dtype, dev,
+                  stream):
     """Gradient buffers (given or allocated) and their dtypes.  A given
     buffer's dtype decides; an explicit dtype that disagrees with it raises."""
     torch = _torch()
@@ -270,9 +290,9 @@ def _grad_outputs(out, need_dh, need_dw, need_db, N, D, V, op_dtype, dh_dtype, d
     dh_dtype = op_dtype if dh_dtype is None else dh_dtype
     dw_dtype = torch.float32 if dw_dtype is None else dw_dtype
     if out is None:
-        dh = torch.empty(N, D, dtype=dh_dtype, device=dev) if need_dh else None
-        dW = torch.empty(V, D, dtype=dw_dtype, device=dev) if need_dw else None
-        db = torch.empty(V, dtype=dw_dtype, device=dev) if need_db else None
+        dh = _new((N, D), dh_dtype, dev, stream) if need_dh else None
+        dW = _new((V, D), dw_dtype, dev, stream) if need_dw else None
+        db = _new((V,), dw_dtype, dev, stream) if need_db else None
     if need_dh:
         _need(dh, "grad_hidden", (N, D), dh_dtype, dev)
     if need_dw:
@@ -291,15 +311,15 @@ def forward(hidden, weight, bias, targets, *, temperature=1.0, workspace=None, o
     N, D, V, dev = _check_linear(hidden, weight, bias, targets)
     code = _code(hidden.dtype)
     if out is None:
-        logp = torch.empty(N, dtype=torch.float32, device=dev)
-        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        logp = _new((N,), torch.float32, dev, stream)
+        lse = _new((N,), torch.float32, dev, stream)
     else:
         logp, lse = out
     _need(logp, "logp", (N,), torch.float32, dev)
     _need(lse, "lse", (N,), torch.float32, dev)
     ws_need = L.ll_workspace_size(N, D, V, code, 0, 0, 0)
     if workspace is None:
-        workspace = _workspace(ws_need, dev)
+        workspace = _workspace(ws_need, dev, stream)
     _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
     st = L.ll_forward_ex(_ptr(hidden), _ptr(weight), _ptr(bias), _ptr(targets), N, D, V, code,
                          _ptr(logp), _ptr(lse), _ptr(workspace), workspace.numel(),
@@ -324,11 +344,12 @@ def backward(grad_logp, hidden, weight, bias, targets, lse, *, need_dh=True, nee
     _need(grad_logp, "grad_logp", (N,), torch.float32, dev)
     _need(lse, "lse", (N,), torch.float32, dev)
     dh, dW, db, dh_dtype, dw_dtype = _grad_outputs(out, need_dh, need_dw, need_db, N, D, V,
-                                                   hidden.dtype, dh_dtype, dw_dtype, dev)
+                                                   hidden.dtype, dh_dtype, dw_dtype, dev,
+                                                   stream)
     ws_need = L.ll_workspace_size(N, D, V, code, token_chunks, 1,
                                   int(bool(need_db)) | (_split_code(split_s) << 1))
     if workspace is None:
-        workspace = _workspace(ws_need, dev)
+        workspace = _workspace(ws_need, dev, stream)
     _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
     st = L.ll_backward_ex(_ptr(grad_logp), _ptr(hidden), _ptr(weight), _ptr(bias),
                           _ptr(targets), _ptr(lse), N, D, V, code, int(bool(need_dh)),
@@ -356,17 +377,18 @@ def forward_backward(grad_logp, hidden, weight, bias, targets, *, need_dh=True, 
         logp, lse, dh, dW, db = out
         grads = (dh, dW, db)
     else:
-        logp = torch.empty(N, dtype=torch.float32, device=dev)
-        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        logp = _new((N,), torch.float32, dev, stream)
+        lse = _new((N,), torch.float32, dev, stream)
         grads = None
     _need(logp, "logp", (N,), torch.float32, dev)
     _need(lse, "lse", (N,), torch.float32, dev)
     dh, dW, db, dh_dtype, dw_dtype = _grad_outputs(grads, need_dh, need_dw, need_db, N, D, V,
-                                                   hidden.dtype, dh_dtype, dw_dtype, dev)
+                                                   hidden.dtype, dh_dtype, dw_dtype, dev,
+                                                   stream)
     ws_need = L.ll_workspace_size(N, D, V, code, token_chunks, 2,
                                   int(bool(need_db)) | (_split_code(split_s) << 1))
     if workspace is None:
-        workspace = _workspace(ws_need, dev)
+        workspace = _workspace(ws_need, dev, stream)
     _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
     st = L.ll_forward_backward_ex(_ptr(grad_logp), _ptr(hidden), _ptr(weight), _ptr(bias),
                                   _ptr(targets), N, D, V, code, _ptr(logp), _ptr(lse),
@@ -390,8 +412,8 @@ def logits_fwd(logits, targets, V=None, *, temperature=1.0, out=None, stream=Non
           dtypes=(torch.float32, torch.float16, torch.bfloat16))
     _need(targets, "targets", (N,), torch.int64, dev)
     if out is None:
-        logp = torch.empty(N, dtype=torch.float32, device=dev)
-        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        logp = _new((N,), torch.float32, dev, stream)
+        lse = _new((N,), torch.float32, dev, stream)
     else:
         logp, lse = out
     _need(logp, "logp", (N,), torch.float32, dev)
@@ -416,7 +438,7 @@ def logits_bwd(grad_logp, logits, targets, lse, V=None, *, temperature=1.0, out=
     _need(grad_logp, "grad_logp", (N,), torch.float32, dev)
     _need(lse, "lse", (N,), torch.float32, dev)
     if out is None:
-        out = torch.empty_like(logits)
+        out = _new((N, ld), logits.dtype, dev, stream)
     _need(out, "grad_logits", (N, ld), logits.dtype, dev)
     st = L.logits_logp_bwd_ex(_ptr(grad_logp), _ptr(logits), ld, _code(logits.dtype),
                               _ptr(targets), _ptr(lse), N, V, _ptr(out), _opts(temperature),
@@ -462,9 +484,9 @@ def logits_fwd_bwd(grad_logp, logits, targets, V=None, *, temperature=1.0, out=N
     _need(targets, "targets", (N,), torch.int64, dev)
     _need(grad_logp, "grad_logp", (N,), torch.float32, dev)
     if out is None:
-        logp = torch.empty(N, dtype=torch.float32, device=dev)
-        lse = torch.empty(N, dtype=torch.float32, device=dev)
-        g = torch.empty_like(logits)
+        logp = _new((N,), torch.float32, dev, stream)
+        lse = _new((N,), torch.float32, dev, stream)
+        g = _new((N, ld), logits.dtype, dev, stream)
     else:
         logp, lse, g = out
     _need(logp, "logp", (N,), torch.float32, dev)
@@ -487,7 +509,7 @@ def sum_ordered(parts, out=None, stream=None):
         raise ValueError("parts must be a CUDA tensor [nparts, n] with contiguous rows")
     k, n = parts.shape
     if out is None:
-        out = torch.empty(n, dtype=parts.dtype, device=parts.device)
+        out = _new((n,), parts.dtype, parts.device, stream)
     _need(out, "out", (n,), parts.dtype, parts.device)
     st = L.ll_sum_ordered(_ptr(parts), k, n, parts.stride(0), _code(parts.dtype), _ptr(out),
                           _stream(stream))
@@ -519,16 +541,17 @@ def forward_shard(hidden, weight, bias, targets, v0, V, *, temperature=1.0, work
     code = _code(hidden.dtype)
     S = shard_segments(Vs)
     if out is None:
-        part_m = torch.empty(S, N, dtype=torch.float32, device=dev)
-        part_s = torch.empty(S, N, dtype=torch.float32, device=dev)
-        zy = torch.empty(N, dtype=torch.float32, device=dev)
+        part_m = _new((S, N), torch.float32, dev, stream)
+        part_s = _new((S, N), torch.float32, dev, stream)
+        zy = _new((N,), torch.float32, dev, stream)
     else:
         part_m, part_s, zy = out
     _need(part_m, "part_m", (S, N), torch.float32, dev)
     _need(part_s, "part_s", (S, N), torch.float32, dev)
     _need(zy, "zy", (N,), torch.float32, dev)
     if workspace is None:
-        workspace = _workspace(L.ll_workspace_size_shard(N, D, Vs, code, 0, 0, 0), dev)
+        workspace = _workspace(L.ll_workspace_size_shard(N, D, Vs, code, 0, 0, 0), dev,
+                               stream)
     _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
     st = L.ll_forward_shard(_ptr(hidden), _ptr(weight), _ptr(bias), _ptr(targets), N, D, Vs,
                             int(v0), int(V), code, _ptr(part_m), _ptr(part_s), _ptr(zy),
@@ -552,8 +575,8 @@ def lse_merge(part_m, part_s, zy, targets, V, *, out=None, stream=None):
     _need(zy, "zy", (N,), torch.float32, dev)
     _need(targets, "targets", (N,), torch.int64, dev)
     if out is None:
-        logp = torch.empty(N, dtype=torch.float32, device=dev)
-        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        logp = _new((N,), torch.float32, dev, stream)
+        lse = _new((N,), torch.float32, dev, stream)
     else:
         logp, lse = out
     _need(logp, "logp", (N,), torch.float32, dev)
@@ -581,10 +604,12 @@ def backward_shard(grad_logp, hidden, weight, bias, targets, lse, v0, V, *, need
     _need(grad_logp, "grad_logp", (N,), torch.float32, dev)
     _need(lse, "lse", (N,), torch.float32, dev)
     dh, dW, db, dh_dtype, dw_dtype = _grad_outputs(out, need_dh, need_dw, need_db, N, D, Vs,
-                                                   hidden.dtype, dh_dtype, dw_dtype, dev)
+                                                   hidden.dtype, dh_dtype, dw_dtype, dev,
+                                                   stream)
     if workspace is None:
         workspace = _workspace(L.ll_workspace_size_shard(
-            N, D, Vs, code, token_chunks, 1, int(bool(need_db)) | (_split_code(split_s) << 1)), dev)
+            N, D, Vs, code, token_chunks, 1, int(bool(need_db)) | (_split_code(split_s) << 1)),
+            dev, stream)
     _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
     st = L.ll_backward_shard(_ptr(grad_logp), _ptr(hidden), _ptr(weight), _ptr(bias),
                              _ptr(targets), _ptr(lse), N, D, Vs, int(v0), int(V), code,
@@ -645,26 +670,6 @@ def _stream_of(device, stream):
     if device.type != "cuda":
         return None  # the call itself then fails: no device memory
     return _torch()._C._cuda_getCurrentRawStream(device.index)
-
-
-def _new(shape, dtype, device, stream, scratch=False):
-    """A new tensor for a call on the current stream, or on `stream`.
-
-    The allocator hands a block that was freed on a stream to that stream alone:
-    work queued there may still use it.  So what `stream` writes comes from its
-    own memory.  The caller may use it on the current stream and then drop it, so
-    the allocator also waits for that one, unless it is scratch of the call."""
-    torch = _torch()
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
-    here = torch.cuda.current_stream(device)
-    if stream == here:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if not scratch:
-        t.record_stream(here)
-    return t
 
 
 def _scratch(workspace, nbytes, device, stream):

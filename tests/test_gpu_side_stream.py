@@ -28,17 +28,36 @@ def calls():
     old, adv = logp + 0.1, torch.randn(N, device="cuda", generator=g)
     offs = torch.tensor([0, 700, N], device="cuda")
     grads = [x, W]
+    h, Wb = x.bfloat16(), (W * D ** -0.5).bfloat16()
+    lse = ll.forward(h, Wb, None, y)[1]
+    z = torch.randn(N, V, device="cuda", generator=g)
+    zl = ll.logits_fwd(z, y)[1]
+    parts = ll.forward_shard(h, Wb, None, y, 0, V)
     return {
         "embed_forward": lambda s: [ll.embed_forward(W, y, stream=s)],
         "embed_backward": lambda s: [ll.embed_backward(x, y, V, stream=s)],
         "policy_loss": lambda s: list(ll.policy_loss(logp, old, adv, seq_offsets=offs, stream=s)),
+        "forward": lambda s: list(ll.forward(h, Wb, None, y, stream=s)),
+        "backward": lambda s: list(ll.backward(adv, h, Wb, None, y, lse, stream=s))[:2],
+        "forward_backward": lambda s: list(ll.forward_backward(adv, h, Wb, None, y, need_db=True,
+                                                               stream=s)),
+        "logits_fwd": lambda s: list(ll.logits_fwd(z, y, stream=s)),
+        "logits_bwd": lambda s: [ll.logits_bwd(adv, z, y, zl, stream=s)],
+        "logits_fwd_bwd": lambda s: list(ll.logits_fwd_bwd(adv, z, y, stream=s)),
+        "forward_shard": lambda s: list(ll.forward_shard(h, Wb, None, y, 0, V, stream=s)),
+        "lse_merge": lambda s: list(ll.lse_merge(*parts, y, V, stream=s)),
+        "backward_shard": lambda s: list(ll.backward_shard(adv, h, Wb, None, y, lse, 0, V,
+                                                           stream=s))[:2],
+        "sum_ordered": lambda s: [ll.sum_ordered(x, stream=s)],
         "grad_norm": lambda s: [ll.grad_norm(grads, stream=s)],
         "clip_grads": lambda s: [ll.clip_grads(grads, float("inf"), stream=s)],
     }
 
 
-@pytest.mark.parametrize("name", ["embed_forward", "embed_backward", "policy_loss", "grad_norm",
-                                  "clip_grads"])
+@pytest.mark.parametrize("name", [
+    "embed_forward", "embed_backward", "policy_loss", "grad_norm", "clip_grads", "forward", "backward",
+    "forward_backward", "logits_fwd", "logits_bwd", "logits_fwd_bwd", "forward_shard", "lse_merge",
+    "backward_shard", "sum_ordered"])
 def test_memory_of_a_call_on_another_stream(lib, monkeypatch, name):
     call = calls()[name]
     want = call(None)

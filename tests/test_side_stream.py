@@ -48,6 +48,14 @@ def test_outputs_come_from_the_stream_that_writes_them(allocations):
     assert t.users == ["current"]  # the caller may drop them while that stream reads
 
 
+def test_gradients_and_workspaces_of_the_linear_calls(allocations, monkeypatch):
+    monkeypatch.setattr(ll, "_need", lambda *a, **k: None)
+    bf16, f32 = torch.bfloat16, torch.float32
+    grads = ll._grad_outputs(None, True, True, True, 4, 8, 16, bf16, None, None, DEVICE, "side")
+    assert [t.pool for t in grads[:3]] == ["side"] * 3 and grads[3:] == (bf16, f32)
+    assert ll._workspace(1000, DEVICE, "side").pool == "side"
+
+
 def test_workspaces_come_from_the_stream_that_uses_them(allocations):
     t = ll._scratch(None, 1000, DEVICE, "side")
     assert t.pool == "side"
