@@ -306,6 +306,7 @@ __global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kThreads)
     __syncthreads();
     if (max_norm > 0.f)
         list_scale(L, blockIdx.x, kSmallCtas, total, max_norm);
+    __syncthreads();  // the cluster's barrier takes whole warps
     cluster_barrier();  // no CTA leaves while another reads its shared memory
 }
 
