@@ -669,7 +669,9 @@ def _stream_of(device, stream):
         return stream.cuda_stream
     if device.type != "cuda":
         return None  # the call itself then fails: no device memory
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+    # a name of torch's own, which other versions may lack: it saves the Stream object
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw else _torch().cuda.current_stream(device).cuda_stream
 
 
 def _scratch(workspace, nbytes, device, stream):

@@ -66,3 +66,16 @@ def test_workspaces_come_from_the_stream_that_uses_them(allocations):
 def test_the_current_stream_needs_nothing(allocations, stream):
     for t in (ll._new((3, 4), torch.float32, DEVICE, stream), ll._scratch(None, 1000, DEVICE, stream)):
         assert t.pool == "current" and t.users == []
+
+
+def test_the_current_stream_without_the_private_getter(monkeypatch):
+    """The handle comes from the public call where torch lacks the quicker one."""
+    class Stream:
+        cuda_stream = 4711
+
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: asked.append(device) or Stream)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert ll._stream_of(DEVICE, None) == 4711 and asked == [DEVICE]
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    assert ll._stream_of(DEVICE, None) == 100 and asked == [DEVICE]
