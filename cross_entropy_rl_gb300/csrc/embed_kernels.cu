@@ -5,7 +5,7 @@
 #include <atomic>
 #include <type_traits>
 
-#include "ll_device.cuh"
+#include "step_device.cuh"
 
 namespace ll {
 namespace {

@@ -10,7 +10,7 @@
 // in L2.  A short list is one launch of one cluster that does both.
 #include <math.h>
 
-#include "ll_device.cuh"
+#include "step_device.cuh"
 
 namespace ll {
 namespace {

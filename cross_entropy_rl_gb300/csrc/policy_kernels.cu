@@ -13,7 +13,7 @@
 // a million in 700 sequences 21.5.
 #include <math.h>
 
-#include "ll_device.cuh"
+#include "step_device.cuh"
 
 namespace ll {
 namespace {
