@@ -108,9 +108,10 @@ constexpr int kStaged = 4096;        // keys a CTA holds in shared memory
 // us, by the cluster 13.5; 4096 tokens 15.8, by the cluster 14.0).
 constexpr int64_t kOneCta = 2048;
 // Most tokens that are matched in one launch instead of sorted.  BF16 added into FP32,
-// matched and sorted: 64 x 4096 3.4 and 10.6 us, 300 x 512 5.5 and 12.2, 1024 x 1024 8.9
-// and 15.7, 1024 x 4096 16.3 and 16.2; with 0.7 of them one token 14.7 and 17.7.  2048 x
-// 256 12.3 and 17.8, but 2048 x 4096 36.8 and 21.4, and with a hot token 30.4 and 20.9.
+// matched and sorted: 64 x 4096 3.8 and 10.9 us, 300 x 512 5.6 and 13.2, 1024 x 1024 9.0
+// and 15.4, 1024 x 4096 16.7 and 16.6; with 0.7 of them one token 14.3 and 17.9.  Of 2048
+// the width decides: 2048 x 256 12.3 and 18.1, but 2048 x 4096 36.8 and 21.4, and with a
+// hot token 30.4 and 20.9.
 constexpr int kMatch = 1024;
 constexpr int kWarpStaged = kStaged / kSortWarps;
 constexpr int kRounds = 4;           // rounds of 32 keys of a warp at a time

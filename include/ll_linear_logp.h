@@ -423,7 +423,8 @@ int ll_sum_ordered(const void* parts, int64_t nparts, int64_t n, int64_t ld, int
  *   tokens [N] int64, device.
  *   out    [N, ld_out] of out_dtype, device (columns [0, D) written, the rest
  *          untouched; ld_out >= D).  out_dtype is dtype, LL_F32, or anything
- *          when dtype is LL_F32.  out may not overlap weight.
+ *          when dtype is LL_F32.  out may not overlap weight, each taken from its
+ *          first element to its last (what lies between two rows included).
  * Pointers need the alignment of their elements only; rows that start on
  * 16-byte boundaries are read and written 16 bytes at a time.
  * scale must be finite.  N == 0 launches nothing.  D >= 1, V >= 1.
@@ -444,11 +445,13 @@ size_t ll_embed_workspace_size(int64_t N, int64_t D, int64_t V);
  *     micro-batches add into one table
  *   grad_out    [N, ldg] dtype, device; ldg >= D.
  *   grad_weight [V, ldw] of dw_dtype (dtype or LL_F32), device (columns
- *               [0, D) written); ldw >= D; it may not overlap grad_out.
- * The rows of one token are added in ascending n, in FP32, in pieces of a
- * fixed number of rows (a function of N alone) whose sums are then added in a
- * fixed order; one rounding to dw_dtype.  A row of grad_weight depends on the
- * rows of its own token alone, and runs give the same bits.
+ *               [0, D) written); ldw >= D; it may not overlap grad_out (as out and
+ *               weight of ll_embed_forward).
+ * The rows of one token are added in ascending n, in FP32, in pieces whose
+ * lengths are a function of N and of the token's own number of rows; the pieces'
+ * sums are then added in an order that is one too; one rounding to dw_dtype.  A
+ * row of grad_weight depends on N and the rows of its own token alone, and runs
+ * give the same bits.
  * N == 0 with accumulate = 0 fills grad_weight with +0.
  */
 int ll_embed_backward(const void* grad_out, int64_t ldg, int dtype, const int64_t* tokens,
@@ -498,8 +501,9 @@ size_t ll_policy_workspace_size(int64_t N, int64_t n_seqs);
  *   stats [4] float, device (written): loss, sum w p, sum w k, sum of w over
  *     the clipped tokens.
  *   grad_logp [N] float, device (written).
- * The clipping border is decided on the exact delta; sums over tokens are held
- * as pairs of FP32 values (about 48 bits) and added in a fixed order.
+ * The clipping border is decided on the exact delta; sums over tokens are plain
+ * FP32 over at most eight of them, pairs of FP32 values (about 48 bits) beyond, and
+ * added in a fixed order.
  * N == 0 writes stats = 0.
  */
 int ll_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,
