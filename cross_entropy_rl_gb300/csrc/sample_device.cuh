@@ -88,7 +88,9 @@ struct Weights {
         const float y = __fmul_rn(r, kLn2Hi);
         const float y_lo = __fmaf_rn(r, kLn2Hi, -y) + __fmaf_rn(r, kLn2Lo, __fmul_rn(a_lo, kLn2Hi));
         const float p = __fmaf_rn(y, __fmaf_rn(y, __fmaf_rn(y, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f);
-        const float q_lo = __fmaf_rn(__fmul_rn(y, y), p, y_lo);
+        // e^y - 1 and y_lo e^y: y_lo is not small enough for y_lo alone (2^-20 where |a| is 17)
+        const float y2 = __fmul_rn(y, y);
+        const float q_lo = __fmaf_rn(y2, p, __fmaf_rn(y_lo, __fmaf_rn(y2, p, y), y_lo));
         const float q = __fadd_rn(y, q_lo), rest_q = __fadd_rn(__fsub_rn(y, q), q_lo);  // e^y - 1
         const float t = __uint_as_float(hi_bits);
         const float u = __fmul_rn(t, q);  // below 0.022
