@@ -1048,7 +1048,6 @@ struct Row {
             // the mass comes to about 2^29
             sh.unit = exp2f(29.f - ceilf(log2f(static_cast<float>(sh.mass))));
             sh.large = exp2f(hi) * sh.unit >= 0x1p21f;
-            sh.n_list = 0;
         }
     }
     // The bin of an exponent x c - ref, rising as it falls, as 1.5 * 2^23 + bin: the integer is
@@ -1242,7 +1241,6 @@ struct Row {
             sh.x_hi = at + kHalf;
             sh.last = (at + sh.ref) / c;
             sh.by_min = 1;
-            sh.n_list = 0;
         }
     }
     // After its split, in the leader.
@@ -1524,7 +1522,11 @@ struct Row {
                     next = kWide;
                 }
                 __syncthreads();
-                if (tid == 0) sh.mode = next;
+                if (tid == 0) {
+                    sh.mode = next;
+                    // only here: until the barrier ahead, others may still have to read it for L
+                    if (next == kWide) sh.n_list = 0;
+                }
             }
             sync();
             mode = at_rank<C>(&sh.mode, 0);
