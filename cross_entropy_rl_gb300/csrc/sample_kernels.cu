@@ -1239,9 +1239,23 @@ struct Row {
                              log2f(fminf(static_cast<float>(sh.set.min_p), 1.f));
             sh.x_lo = at - kHalf;
             sh.x_hi = at + kHalf;
-            sh.last = (at + sh.ref) / c;
             sh.by_min = 1;
         }
+    }
+    // The largest logit whose exponent is not above x_hi, so that `x > last` holds for exactly
+    // the tokens that split() and exact_sums() take as above the piece.  (x_hi + ref) / c, rounded,
+    // is off by more than the piece is wide once |x c| is some thousands.
+    __device__ float last_below() const {
+        const float c = sh.set.c, ref_f = static_cast<float>(sh.ref), hi = sh.x_hi;
+        uint32_t a = key_of(Bounds<T>::low), b = key_of(sh.top);  // the largest is above the piece
+        while (b - a > 1) {
+            const uint32_t mid = a + (b - a) / 2;
+            if (fmaf(value_of(mid), c, -ref_f) > hi)
+                b = mid;
+            else
+                a = mid;
+        }
+        return value_of(a);
     }
     // After its split, in the leader.
     __device__ __forceinline__ Mode draw_min() {
@@ -1269,8 +1283,8 @@ struct Row {
         if (tid == 0) {
             sh.kept = left;
             sh.last_end = 0;
-            // below the list's first if none of it is left
-            if (left == 0 && L > 0) sh.last = value_of(static_cast<uint32_t>(sh.list[0] >> 32));
+            // none of the list is left: those above its first, or above the piece
+            if (left == 0) sh.last = L > 0 ? value_of(static_cast<uint32_t>(sh.list[0] >> 32)) : last_below();
         }
         __syncthreads();
         if (again) return kSums;
@@ -1340,9 +1354,10 @@ struct Row {
                 all = above = 0;
             });
     }
-    // The draw from the sums of each range over the tokens left, sh.range_list.
+    // The draw from the sums of each range over the tokens left, sh.range_list.  Returns false if
+    // the tokens do not add up to these.
     template <bool CUT>
-    __device__ __noinline__ void draw_exact() {
+    __device__ __noinline__ bool draw_exact() {
         const Weights W = weights();
         const float last = sh.last;
         const uint32_t last_end = sh.last_end;
@@ -1352,7 +1367,7 @@ struct Row {
             const double want = sh.set.u * static_cast<double>(total);
             const u64 target = want < static_cast<double>(total) ? static_cast<u64>(want) : total - 1;
             const uint32_t over = __ballot_sync(0xffffffffu, up > target);
-            if (lane == __ffs(over) - 1) {
+            if (lane == (over ? __ffs(over) - 1 : 31)) {
                 const bool second = up - own + first <= target;
                 sh.total = total;
                 sh.target = target;
@@ -1377,37 +1392,45 @@ struct Row {
             if (lane == 0) sh.gsum[g - g0] = sum;
         }
         __syncthreads();
-        if (warp != 0) return;
-        u64 before = sh.ahead;
-        const u64 target = sh.target;
-        for (int g = g0; g < g1; g += 32) {
-            const u64 own = g + lane < g1 ? sh.gsum[g + lane - g0] : 0, up = scan_up64(own);
-            const uint32_t over = __ballot_sync(0xffffffffu, before + up > target);
-            if (over == 0) {
-                before += __shfl_sync(0xffffffffu, up, 31);
-                continue;
-            }
-            const int at = __ffs(over) - 1;
-            before += __shfl_sync(0xffffffffu, up - own, at);
-            g += at;
-            float f[8];
-            load(g).get(f);
-            u64 w[8], sum = 0;
+        if (warp == 0) {
+            u64 before = sh.ahead;
+            const u64 target = sh.target;
+            bool here = false;
+            for (int g = g0; g < g1; g += 32) {
+                const u64 own = g + lane < g1 ? sh.gsum[g + lane - g0] : 0, up = scan_up64(own);
+                const uint32_t over = __ballot_sync(0xffffffffu, before + up > target);
+                if (over == 0) {
+                    before += __shfl_sync(0xffffffffu, up, 31);
+                    continue;
+                }
+                const int at = __ffs(over) - 1;
+                before += __shfl_sync(0xffffffffu, up - own, at);
+                g += at;
+                float f[8];
+                load(g).get(f);
+                u64 w[8], sum = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                w[j] = left(f[j], g * kGroup + lane * 8 + j) ? W(f[j]) : 0;
-                sum += w[j];
-            }
-            before += scan_up64(sum) - sum;
+                for (int j = 0; j < 8; ++j) {
+                    w[j] = left(f[j], g * kGroup + lane * 8 + j) ? W(f[j]) : 0;
+                    sum += w[j];
+                }
+                before += scan_up64(sum) - sum;
 #pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
-                if (before <= target && before + w[j] > target)
-                    write(int64_t(g) * kGroup + lane * 8 + j, f[j],
-                          log_of(static_cast<double>(sh.total), W.S));
-                before += w[j];
+                for (int j = 0; j < 8; ++j) {
+                    if (before <= target && before + w[j] > target) {
+                        write(int64_t(g) * kGroup + lane * 8 + j, f[j],
+                              log_of(static_cast<double>(sh.total), W.S));
+                        here = true;
+                    }
+                    before += w[j];
+                }
+                break;
             }
-            return;
+            here = __any_sync(0xffffffffu, here);
+            if (lane == 0) sh.count = here;
         }
+        __syncthreads();
+        return sh.count != 0;
     }
     // After exact_sums, in the leader.  WAS: what could not be decided.
     __device__ __forceinline__ bool decide_exact(Mode was) {
@@ -1430,12 +1453,9 @@ struct Row {
             const int left = sh.by_min ? sh.kept : border();
             if (left < 1 && !sh.by_min) return false;
             keep_list(left);
-            draw_exact<true>();
-        } else {
-            draw_exact<false>();
+            return draw_exact<true>();
         }
-        __syncthreads();
-        return true;
+        return draw_exact<false>();
     }
     __device__ __noinline__ bool run_exact(Mode was) {
         exact_sums(was == kWide);
