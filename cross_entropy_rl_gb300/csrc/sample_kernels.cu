@@ -1023,7 +1023,8 @@ struct Row {
                     for (int j = 0; j < 8; ++j)
                         in |= f[j] >= floor_x && f[j] > Bounds<T>::low ? 1u << j : 0u;
                     int at = take(__popc(in));
-                    full = __any_sync(0xffffffffu, at >= kList);
+                    // past its end: after exactly kList tokens the next ones still have to show
+                    full = __any_sync(0xffffffffu, at > kList);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if ((in >> j) & 1u) append(at++, f[j], g * kGroup + lane * 8 + j);
