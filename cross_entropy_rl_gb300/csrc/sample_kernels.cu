@@ -560,14 +560,19 @@ struct Row {
         sh.scale = exp2(sh.ref - static_cast<double>(top) * set.c);
         sh.log_z = log_of(Z * sh.scale);
         sh.one = static_cast<double>(1ull << weight_bits(V));
-        // A floor under the tokens left, a little lower than the bounds: they are rounded
+        // A floor under the tokens left, a little lower than the bounds: these are sums of rounded
+        // numbers, and off by a few 2^-24 of each where they cancel (and where a logarithm is near
+        // 0, of one unit of it).
         float at = -INFINITY;
-        auto lower = [](float x) { return x - 1e-4f * fabsf(x) - 1e-30f; };
+        auto lower = [](float x, float y, float unit) {
+            const float sum = x + y;
+            return sum - 1e-4f * fabsf(sum) - 1e-6f * (fabsf(x) + fabsf(y) + unit);
+        };
         if (set.k >= V && set.p < 1) {
             // all that lies below weight w_f weighs less than V w_f = (1 - p) Z
             const double m = set.p * Z;
             const float w_f = static_cast<float>(Z - m) * (1.f - 2.f * E) / static_cast<float>(V);
-            if (w_f > 1e-30f) at = lower((log2f(w_f) + ref) / set.c);
+            if (w_f > 1e-30f) at = lower(log2f(w_f), static_cast<float>(ref), 1.f) / set.c;
             const double scale = sh.scale * sh.one;
             sh.p_lo = m * scale * (1.0 - E) - 2.0 * kList;  // the list's weights are rounded
             sh.p_hi = m * scale * (1.0 + E) + 2.0 * kList;
@@ -576,7 +581,8 @@ struct Row {
         if (set.min_p > 0) {
             const double r_min = fmin(set.min_p, 1.0);
             if (r_min > 1e-30 && !(set.k < V && set.p < 1))  // top_p is of the whole top_k's mass
-                at = fmaxf(at, lower(top + logf(static_cast<float>(r_min)) * static_cast<float>(set.T)));
+                at = fmaxf(at, lower(top, logf(static_cast<float>(r_min)) * static_cast<float>(set.T),
+                                     static_cast<float>(set.T)));
             sh.least = static_cast<u64>(ceil(r_min * sh.one));
         }
         sh.per_one = 1.0 / (sh.scale * sh.one);
