@@ -82,6 +82,10 @@ struct RowX {
     bool vec;
     Weights W;
     u64 least;
+    // u of 1 or more takes the last token left, also where its weight is no whole unit: tokens
+    // then count 1 each, and min_p is compared with x - max in FP64
+    bool by_count;
+    double floor_d;
 
     __device__ __forceinline__ void sync() const {
         __syncthreads();
@@ -219,8 +223,28 @@ struct RowX {
         const uint32_t key = key_of(x);
         ties += key == last;
         if (key <= last) return 0;
+        if (by_count) return counts(x) ? 1 : 0;
         const u64 w = W(x);
         return w >= least ? w : 0;
+    }
+    __device__ __forceinline__ bool counts(float x) const {
+        return x == W.m || (W.m < INFINITY && static_cast<double>(x) - W.m >= floor_d);
+    }
+    // Sums over the tokens left, a run of groups each, to the leader.
+    __device__ __forceinline__ void sum_left(uint32_t last, uint32_t to_sum, uint32_t to_ties) const {
+        uint32_t ties = 0;
+        u64 sum = 0;
+        stream([&](const float (&f)[8]) {
+#pragma unroll 4
+            for (int j = 0; j < 8; ++j) sum += above_last(f[j], last, ties);
+        });
+        sum = warp_sum64(sum);
+        ties = __reduce_add_sync(0xffffffffu, last ? ties : 0u);
+        if (lane == 0) {
+            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_sum), "l"(sum) : "memory");
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to_ties), "r"(ties) : "memory");
+        }
+        sync();
     }
 
     __device__ __forceinline__ void run() {
@@ -294,28 +318,22 @@ struct RowX {
         if (set.min_p > 0)
             least = static_cast<u64>(ceil(fmin(set.min_p, 1.0) * static_cast<double>(1ull << W.S)));
         const u64 w_last = last ? W(value_of(last)) : 0;
-        const u64 w_tie = w_last >= least ? w_last : 0;
-        if (last || least) {  // sums over the tokens left, a run of groups each
-            uint32_t ties = 0;
-            sum = 0;
-            stream([&](const float (&f)[8]) {
-#pragma unroll 4
-                for (int j = 0; j < 8; ++j) sum += above_last(f[j], last, ties);
-            });
-            sum = warp_sum64(sum);
-            ties = __reduce_add_sync(0xffffffffu, last ? ties : 0u);
-            if (lane == 0) {
-                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_sum), "l"(sum) : "memory");
-                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to_ties), "r"(ties) : "memory");
-            }
+        u64 w_tie = w_last >= least ? w_last : 0;
+        if (last || least) sum_left(last, to_sum, to_ties);
+        if (set.u >= 1) {
+            if (rank == 0) find_run(n_last, w_tie);  // their mass
             sync();
+            by_count = true;
+            floor_d = set.min_p > 0 && set.T < INFINITY ? set.T * log(fmin(set.min_p, 1.0)) : -INFINITY;
+            w_tie = last && counts(value_of(last)) ? 1 : 0;
+            sum_left(last, to_sum, to_ties);
         }
         if (rank == 0) draw(every, last, n_last, w_tie);
         sync();
     }
 
-    // The leader: the run, the group and the token that the target lies in.
-    __device__ __forceinline__ void draw(u64 every, uint32_t last, uint32_t n_last, u64 w_tie) {
+    // The leader: the run that the target lies in.
+    __device__ __forceinline__ void find_run(uint32_t n_last, u64 w_tie) {
         const Settings& set = sh.set;
         if (warp == 0) {  // a lane: 4 runs
             constexpr int kEach = kRuns / 32;
@@ -358,11 +376,16 @@ struct RowX {
                     sh.before = at;
                     sh.ties_before = ahead[i];
                     sh.target = target;
-                    sh.total = total;
+                    if (!by_count) sh.total = total;
                 }
                 at += own[i];
             }
         }
+    }
+    // The leader: the run, the group and the token that the target lies in.
+    __device__ __forceinline__ void draw(u64 every, uint32_t last, uint32_t n_last, u64 w_tie) {
+        const Settings& set = sh.set;
+        find_run(n_last, w_tie);
         __syncthreads();
         const u64 target = sh.target;
         u64 before = sh.before;
@@ -456,7 +479,7 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kThreadsX, 2)
             if (tid == 0) sh.set = settings_of(a, n);
             const T* row = static_cast<const T*>(a.logits) + n * a.ld;
             RowX<T> r{a, sh, row, n, a.V, (a.V + kGroupX - 1) / kGroupX, per, rank, tid, tid >> 5, tid & 31,
-                      reinterpret_cast<uintptr_t>(row) % 16 == 0, {}, 0};
+                      reinterpret_cast<uintptr_t>(row) % 16 == 0, {}, 0, false, 0.0};
             r.run();
         }
     }
