@@ -80,6 +80,10 @@ struct RowX {
     int64_t n, V, G, per;
     int rank, tid, warp, lane;
     bool vec;
+    float m;  // the largest
+    // At temperatures above 2^60 logits are taken as 2^-64 of themselves, and c as 2^64 of itself: the
+    // distance of two logits that weighs something may not fit FP32, nor c
+    float part;
     Weights W;
     u64 least;
     // u of 1 or more takes the last token left, also where its weight is no whole unit: tokens
@@ -151,7 +155,7 @@ struct RowX {
                     if (key && (bits == 32 || key >> bits == prefix)) {
                         const uint32_t bin = (key >> shift) & ((1u << (bits - shift)) - 1);
                         atomicAdd(&sh.own.count[bin], 1u);
-                        atomicAdd(&sh.own.mass[bin], W(f[j]));
+                        atomicAdd(&sh.own.mass[bin], weight(f[j]));
                     }
                 }
             });
@@ -218,17 +222,18 @@ struct RowX {
         return true;
     }
 
+    __device__ __forceinline__ u64 weight(float x) const { return W(x * part); }
     // Weight of the token if it is left, equal ones counted apart.
     __device__ __forceinline__ u64 above_last(float x, uint32_t last, uint32_t& ties) const {
         const uint32_t key = key_of(x);
         ties += key == last;
         if (key <= last) return 0;
         if (by_count) return counts(x) ? 1 : 0;
-        const u64 w = W(x);
+        const u64 w = weight(x);
         return w >= least ? w : 0;
     }
     __device__ __forceinline__ bool counts(float x) const {
-        return x == W.m || (W.m < INFINITY && static_cast<double>(x) - W.m >= floor_d);
+        return x == m || (m < INFINITY && static_cast<double>(x) - m >= floor_d);
     }
     // Sums over the tokens left, a run of groups each, to the leader.
     __device__ __forceinline__ void sum_left(uint32_t last, uint32_t to_sum, uint32_t to_ties) const {
@@ -270,16 +275,24 @@ struct RowX {
             }
             return;
         }
-        W.m = value_of(top);
+        m = value_of(top);
         W.c_hi = set.c;
         W.c_lo = set.c_lo;
+        part = 1.f;
+        if (set.cd < 0x1p-60) {
+            const double c = set.cd * 0x1p64;
+            W.c_hi = static_cast<float>(c);
+            W.c_lo = static_cast<float>(c - W.c_hi);
+            part = 0x1p-64f;
+        }
+        W.m = m * part;
         W.S = weight_bits(V);
         W.tab = smem_u32(sh.tab);
         u64 sum = 0;
         stream([&](const float (&f)[8]) {
 #pragma unroll 4
             for (int j = 0; j < 8; ++j)
-                if (key_of(f[j])) sum += W(f[j]);
+                if (key_of(f[j])) sum += weight(f[j]);
         });
         sum = warp_sum64(sum);
         const int own_run = rank * kWarpsX + warp;
@@ -297,14 +310,14 @@ struct RowX {
         if (set.k < V && select<false>(static_cast<u64>(set.k))) {
             last = ld_leader(&sh.prefix);
             n_last = static_cast<uint32_t>(set.k) - ld_leader(&sh.above_count);
-            mass = ld_leader(&sh.above_mass) + W(value_of(last)) * n_last;
+            mass = ld_leader(&sh.above_mass) + weight(value_of(last)) * n_last;
             sync();
         }
         if (set.p < 1) {
             const u64 need = static_cast<u64>(fmax(ceil(set.p * static_cast<double>(mass)), 1.0));
             if (select<true>(need)) {
                 const uint32_t at = ld_leader(&sh.prefix);
-                const u64 w = W(value_of(at));
+                const u64 w = weight(value_of(at));
                 const uint32_t some =
                     w ? static_cast<uint32_t>((need - ld_leader(&sh.above_mass) + w - 1) / w) : 1u;
                 if (at > last || (at == last && some < n_last)) {
@@ -317,7 +330,7 @@ struct RowX {
         least = 0;
         if (set.min_p > 0)
             least = static_cast<u64>(ceil(fmin(set.min_p, 1.0) * static_cast<double>(1ull << W.S)));
-        const u64 w_last = last ? W(value_of(last)) : 0;
+        const u64 w_last = last ? weight(value_of(last)) : 0;
         u64 w_tie = w_last >= least ? w_last : 0;
         if (last || least) sum_left(last, to_sum, to_ties);
         if (set.u >= 1) {
@@ -444,7 +457,7 @@ struct RowX {
                 at += s;
                 if (at > target) {
                     const float x = f[j];
-                    const double z = x == W.m ? 0.0 : (static_cast<double>(x) - W.m) / set.T;
+                    const double z = x == m ? 0.0 : (static_cast<double>(x) - m) / set.T;
                     const double one = static_cast<double>(1ull << W.S);
                     a.tokens[n] = g * kGroupX + lane * 8 + j;
                     a.logp[n] = static_cast<float>(z - log(static_cast<double>(every) / one));
@@ -479,7 +492,7 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kThreadsX, 2)
             if (tid == 0) sh.set = settings_of(a, n);
             const T* row = static_cast<const T*>(a.logits) + n * a.ld;
             RowX<T> r{a, sh, row, n, a.V, (a.V + kGroupX - 1) / kGroupX, per, rank, tid, tid >> 5, tid & 31,
-                      reinterpret_cast<uintptr_t>(row) % 16 == 0, {}, 0, false, 0.0};
+                      reinterpret_cast<uintptr_t>(row) % 16 == 0, 0.f, 1.f, {}, 0, false, 0.0};
             r.run();
         }
     }
