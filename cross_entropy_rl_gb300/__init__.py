@@ -1041,11 +1041,11 @@ def fp4_dequantize(q, out_dtype=None, *, out=None, stream=None):
         _is_fp4(q, "q")
     codes, K = q.codes, q.cols
     R, dev = codes.shape[0], codes.device
-    out, ldo = _out_2d(out, out_dtype, _TORCH.float32, (R, K), dev, stream)
+    out, ldo = _out_2d(out, out_dtype, _torch().float32, (R, K), dev, stream)
     scale = q.scale
     st = L.ll_fp4_dequantize(codes.data_ptr(), q.scales.data_ptr(),
                              None if scale is None else scale.data_ptr(), R, K,
-                             FP4_FORMATS[q.format], out.data_ptr(), ldo, _CODES[out.dtype],
+                             FP4_FORMATS[q.format], out.data_ptr(), ldo, _codes()[out.dtype],
                              _stream_of(dev, stream))
     if st:
         raise LLError("ll_fp4_dequantize", st)
