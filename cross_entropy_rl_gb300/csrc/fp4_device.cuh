@@ -58,6 +58,19 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
     return __uint_as_float(bits);
 }
 
+// The product of two matrices' scales as g * two, `two` a power of 2: 1 where the product lies
+// within 2^-100 .. 2^100.  A sum of products, 0 or 2^-20 to 2^54 in size, times `two` and then g
+// leaves FP32's range only where it does so times both scales (and then by 2^-126 at least).
+struct ScaleProduct {
+    float g, two;
+};
+__device__ __forceinline__ ScaleProduct scale_product(float h, float w) {
+    int eh, ew;
+    const float m = frexpf(h, &eh) * frexpf(w, &ew);
+    const int e = eh + ew, near = min(max(e, -100), 100);
+    return {ldexpf(m, near), ldexpf(1.f, min(max(e - near, -126), 127))};
+}
+
 // Byte of block scale `b` of row r.
 __device__ __forceinline__ int64_t scale_at(int64_t r, int64_t b, int64_t k_tiles) {
     return ((r / kFp4TileRows) * k_tiles + b / kFp4TileBlocks) * kFp4TileBytes + (r % 32) * 16 +

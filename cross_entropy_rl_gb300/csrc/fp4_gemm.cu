@@ -314,7 +314,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         int buf = 0;
         uint32_t bphase = 0;
         bool ok = true;
-        const float g = FORMAT == LL_FP4_NV ? *P.h_scale * *P.w_scale : 1.f;
+        ScaleProduct scale = {1.f, 1.f};
+        if (FORMAT == LL_FP4_NV) scale = scale_product(*P.h_scale, *P.w_scale);
+        const float g = scale.g;
         T* out = static_cast<T*>(P.out);
         for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
             const int64_t v = t * 128 + q * 32 + lane;
@@ -331,6 +333,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 __syncwarp();
                 tmem_ld32(taddr + c, r);
                 tmem_ld_wait(r);
+                if (FORMAT == LL_FP4_NV && scale.two != 1.f) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale.two);
+                }
                 if (v < P.V) {
                     T* o = out + int64_t(c) * P.ldo + v;
                     const int left = static_cast<int>(min(int64_t(32), P.N - c));
@@ -628,7 +634,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int sw = lane & 7;
         uint32_t tphase = 0;
         bool ok = true;
-        const float g = FORMAT == LL_FP4_NV ? *P.h_scale * *P.w_scale : 1.f;
+        ScaleProduct scale = {1.f, 1.f};
+        if (FORMAT == LL_FP4_NV) scale = scale_product(*P.h_scale, *P.w_scale);
+        const float g = scale.g;
         constexpr int kCols = 128 / int(sizeof(T));  // of a box
         const bool wide = P.wide_out != 0;
         T* out = static_cast<T*>(P.out);
@@ -650,6 +658,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
                 tmem_ld32(taddr + c * 32, r);
                 tmem_ld_wait(r);
+                if (FORMAT == LL_FP4_NV && scale.two != 1.f) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale.two);
+                }
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
