@@ -101,6 +101,30 @@ __device__ __forceinline__ float load_bias(const void* b, int dtype, int64_t v) 
     return __bfloat162float(static_cast<const __nv_bfloat16*>(b)[v]);
 }
 
+// Which stages a producer has loaded, and the phase of their barriers that each load completes.
+struct Issued {
+    uint32_t stages = 0, phases = 0;
+    __device__ __forceinline__ void add(int stage, uint32_t phase) {
+        stages |= 1u << stage;
+        phases = (phases & ~(1u << stage)) | (phase << stage);
+    }
+};
+// Waits, up to one limit in all, for those stages' barriers; returns the stages still on their way.
+// By a whole warp, which stays together.
+__device__ __forceinline__ uint32_t wait_for_loads(uint64_t* bars, const Issued& issued,
+                                                   uint64_t limit_ns) {
+    uint32_t left = issued.stages;
+    const uint64_t t0 = globaltimer_ns();
+    while (left) {
+        for (int s = 0; s < kMaxStages; ++s)
+            if (((left >> s) & 1u) &&
+                __all_sync(0xffffffffu, mbar_try_wait_cl(&bars[s], (issued.phases >> s) & 1u)))
+                left &= ~(1u << s);
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) break;
+    }
+    return left;
+}
+
 struct GemmArgs {
     const uint8_t *h_scales, *w_scales;
     const float *h_scale, *w_scale;
@@ -172,7 +196,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     if (warp == 0) {
         // ------------------------------------------------------- producer
         int stage = 0;
-        uint32_t phase = 0, issued = 0, issued_phase = 0;
+        uint32_t phase = 0;
+        Issued issued;
         bool ok = true;
         for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             for (int64_t kb = 0; kb < k_stages; ++kb) {
@@ -197,8 +222,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                     bulk_load(ss + F::kScaleBytes, P.h_scales + st0 * kFp4TileBytes, sb, bar);
                 }
                 __syncwarp();
-                issued |= 1u << stage;
-                issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                issued.add(stage, phase);
                 if (++stage == stages) {
                     stage = 0;
                     phase ^= 1;
@@ -208,10 +232,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         if (!ok) {
             if (lane == 0) set_status(P.status, LL_ERR_DEVICE_TIMEOUT);
             bars.abort = 1;
-            for (int s = 0; s < stages; ++s)
-                if ((issued >> s) & 1u)
-                    mbar_wait(&bars.full[s], (issued_phase >> s) & 1u, P.wait_ns, nullptr);
         }
+        // no load is in flight when the CTA ends, whichever warp gave up
+        wait_for_loads(bars.full, issued, P.wait_ns);
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
         int stage = 0, buf = 0;
@@ -480,6 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // ------------------------------------------------------- producer
         int stage = 0;
         uint32_t phase = 0;
+        Issued issued;
         bool ok = true;
         const uint32_t full0 = cluster_addr(&bars.full[0], 0);
         for (int64_t t = pair; t < tiles && ok; t += pairs) {
@@ -514,6 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                   &bars.landed[stage]);
                 }
                 __syncwarp();
+                issued.add(stage, phase);
                 if (++stage == kPairStages) {
                     stage = 0;
                     phase ^= 1;
@@ -523,6 +548,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!ok) {
             if (lane == 0) set_status(P.status, LL_ERR_DEVICE_TIMEOUT);
             bars.abort = 1;
+        }
+        // No load is in flight when the CTAs end, whichever warp gave up: each waits for its scales,
+        // the leader for both CTAs' tiles, which are counted there, and for the next ones of the
+        // other, which may have loaded on where this one stopped.  (Both end together, below.)
+        wait_for_loads(bars.landed, issued, P.wait_ns);
+        if (leader) {
+            const uint32_t late = wait_for_loads(bars.full, issued, P.wait_ns);
+            if (!ok) {
+                Issued other;
+                for (int s = 0; s < kPairStages; ++s)
+                    if (!((late >> s) & 1u)) {
+                        if (lane == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * kTileBytes);
+                        other.add(s, (issued.stages >> s) & 1u ? ((issued.phases >> s) & 1u) ^ 1u : 0u);
+                    }
+                __syncwarp();
+                wait_for_loads(bars.full, other, P.wait_ns);
+            }
         }
     } else if (warp == 1) {
         // ------------------------------------------- MMA issuer (leader only)
