@@ -230,10 +230,10 @@ class Clocks:
 # source files each timed kernel is built from (a change to any of them
 # invalidates a stored ncu traffic figure for that kernel)
 KERNEL_SOURCES = {
-    "gemm": ["gemm_tc.cu", "gemm_common.cuh", "epilogue.cuh", "ll_device.cuh", "ll_internal.h",
-             "capi.cu"],
-    "gemm_f32": ["gemm_tf32.cu", "gemm_tc.cu", "gemm_common.cuh", "epilogue.cuh", "ll_device.cuh",
-                 "ll_internal.h", "capi.cu"],
+    "gemm": ["gemm_tc.cu", "gemm_common.cuh", "loads_device.cuh", "epilogue.cuh", "ll_device.cuh",
+             "ll_internal.h", "capi.cu"],
+    "gemm_f32": ["gemm_tf32.cu", "gemm_tc.cu", "gemm_common.cuh", "loads_device.cuh", "epilogue.cuh",
+                 "ll_device.cuh", "ll_internal.h", "capi.cu"],
     "logits": ["logits_kernels.cu", "ll_device.cuh", "ll_internal.h"],
 }
 PHASE_SOURCES = {"fwd_gemm": "gemm", "recompute_gemm": "gemm", "grad_gemm": "gemm",

@@ -27,7 +27,7 @@ SOURCES = ["capi.cu", "capi_step.cu", "logits_kernels.cu", "gemm_tc.cu", "gemm_t
            "sample_exact.cu"]
 HEADERS = ["ll_device.cuh", "ll_internal.h", "capi_common.h", "step_device.cuh", "step_internal.h",
            "epilogue.cuh", "gemm_common.cuh", "rollout_internal.h", "fp4_device.cuh",
-           "sample_device.cuh"]
+           "sample_device.cuh", "loads_device.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

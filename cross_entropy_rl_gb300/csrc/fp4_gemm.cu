@@ -24,6 +24,7 @@
 #include <mutex>
 
 #include "fp4_device.cuh"
+#include "loads_device.cuh"
 
 namespace ll {
 namespace {
@@ -99,30 +100,6 @@ __device__ __forceinline__ float load_bias(const void* b, int dtype, int64_t v) 
     if (dtype == LL_F32) return static_cast<const float*>(b)[v];
     if (dtype == LL_F16) return __half2float(static_cast<const __half*>(b)[v]);
     return __bfloat162float(static_cast<const __nv_bfloat16*>(b)[v]);
-}
-
-// Which stages a producer has loaded, and the phase of their barriers that each load completes.
-struct Issued {
-    uint32_t stages = 0, phases = 0;
-    __device__ __forceinline__ void add(int stage, uint32_t phase) {
-        stages |= 1u << stage;
-        phases = (phases & ~(1u << stage)) | (phase << stage);
-    }
-};
-// Waits, up to one limit in all, for those stages' barriers; returns the stages still on their way.
-// By a whole warp, which stays together.
-__device__ __forceinline__ uint32_t wait_for_loads(uint64_t* bars, const Issued& issued,
-                                                   uint64_t limit_ns) {
-    uint32_t left = issued.stages;
-    const uint64_t t0 = globaltimer_ns();
-    while (left) {
-        for (int s = 0; s < kMaxStages; ++s)
-            if (((left >> s) & 1u) &&
-                __all_sync(0xffffffffu, mbar_try_wait_cl(&bars[s], (issued.phases >> s) & 1u)))
-                left &= ~(1u << s);
-        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) break;
-    }
-    return left;
 }
 
 struct GemmArgs {
@@ -553,19 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // the leader for both CTAs' tiles, which are counted there, and for the next ones of the
         // other, which may have loaded on where this one stopped.  (Both end together, below.)
         wait_for_loads(bars.landed, issued, P.wait_ns);
-        if (leader) {
-            const uint32_t late = wait_for_loads(bars.full, issued, P.wait_ns);
-            if (!ok) {
-                Issued other;
-                for (int s = 0; s < kPairStages; ++s)
-                    if (!((late >> s) & 1u)) {
-                        if (lane == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * kTileBytes);
-                        other.add(s, (issued.stages >> s) & 1u ? ((issued.phases >> s) & 1u) ^ 1u : 0u);
-                    }
-                __syncwarp();
-                wait_for_loads(bars.full, other, P.wait_ns);
-            }
-        }
+        if (leader) wait_for_pair_loads(bars.full, issued, kPairStages, 2 * kTileBytes, !ok, P.wait_ns);
     } else if (warp == 1) {
         // ------------------------------------------- MMA issuer (leader only)
         if (leader) {

@@ -28,6 +28,7 @@
 // changes any result: every output element is one MMA accumulation over K
 // in a fixed order.
 #include "gemm_common.cuh"
+#include "loads_device.cuh"
 
 namespace ll {
 namespace {
@@ -528,6 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------- scheduler (leader) + TMA producer (both CTAs)
         int stage = 0, sslot = 0;
         uint32_t phase = 0, sphase = 0;
+        Issued issued;
         bool ok = true;
         int64_t next_static = pair;
         while (ok) {
@@ -608,6 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                     __syncwarp();
+                    issued.add(stage, phase);
                     if (++stage == kPairStages) {
                         stage = 0;
                         phase ^= 1;
@@ -619,6 +622,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) set_status(status, LL_ERR_DEVICE_TIMEOUT);
             bars->abort = 1;
         }
+        // no load is in flight when the CTAs end, whichever warp gave up
+        if (leader)
+            wait_for_pair_loads(bars->full, issued, kPairStages, kPairStageBytes, !ok, wait_ns);
     } else if (warp == 1) {
         // ------------------------------------------- MMA issuer (leader only)
         if (leader) {

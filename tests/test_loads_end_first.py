@@ -1,6 +1,7 @@
 """A CTA must not end while a load into its shared memory is in flight, also after one of its
-bounded waits ran out: the producers of the 4-bit product keep a record of their loads and
-wait for them, with a limit, before they leave, whichever warp gave up."""
+bounded waits ran out: the producers of the 4-bit product and of the GEMM on CTA pairs keep a
+record of their loads and wait for them, with a limit, before they leave, whichever warp
+gave up."""
 import os
 import re
 
@@ -20,21 +21,26 @@ def block_end(text, at):
     return at
 
 
-@pytest.mark.parametrize("kernel,barriers", [("few_kernel", ["full"]), ("pair_kernel", ["landed", "full"])])
-def test_producers_wait_for_their_loads(kernel, barriers):
-    with open(os.path.join(CSRC, "fp4_gemm.cu")) as f:
+@pytest.mark.parametrize("source,kernel,waits", [
+    ("fp4_gemm.cu", "few_kernel", ["wait_for_loads(bars.full, issued"]),
+    ("fp4_gemm.cu", "pair_kernel", ["wait_for_loads(bars.landed, issued",
+                                    "if (leader) wait_for_pair_loads(bars.full, issued"]),
+    ("gemm_tc.cu", "gemm_pair_kernel", ["if (leader) wait_for_pair_loads(bars->full, issued"]),
+])
+def test_producers_wait_for_their_loads(source, kernel, waits):
+    with open(os.path.join(CSRC, source)) as f:
         code = re.sub(r"//[^\n]*", "", f.read())
-    start = code.index(kernel + "(const __grid_constant__")
+    start = re.search(r"\b%s\(const __grid_constant__" % kernel, code).end()
     start = code.index("if (warp == 0) {", start)
     producer = code[start:block_end(code, start)]
-    loads = producer[producer.index("for ("):]
-    rest = loads[block_end(loads, 0):]
-    loads = loads[:block_end(loads, 0)]
+    at = re.search(r"\b(for|while) \([^{]*\{", producer)
+    loads = producer[at.start():block_end(producer, at.start())]
+    rest = producer[at.start() + len(loads):]
     # every stage that the loop loads is recorded, ahead of the step to the next
-    assert len(re.findall(r"tma_load_2d(?:_pair)?\(", loads)) == 2
-    assert re.search(r"issued\.add\(stage, phase\);\s*if \(\+\+stage == ", loads)
+    assert re.search(r"\w*load\w*(<[^()]*>)?\(", loads)
+    assert [x.strip() for x in re.findall(r"(.*);\s*if \(\+\+stage == ", loads)] == ["issued.add(stage, phase)"]
     # and waited for behind the loop, outside of what runs after a time-out alone
     gave_up = rest.index("if (!ok)")
-    always = rest[:gave_up] + rest[block_end(rest, gave_up):]
-    for name in barriers:
-        assert re.search(r"wait_for_loads\(bars\.%s, issued, P\.wait_ns\)" % name, always)
+    always = re.sub(r"\s+", " ", rest[:gave_up] + rest[block_end(rest, gave_up):])
+    for wait in waits:
+        assert wait in always
