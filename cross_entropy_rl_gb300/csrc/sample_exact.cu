@@ -93,6 +93,7 @@ struct RowX {
 
     __device__ __forceinline__ void sync() const {
         __syncthreads();
+        __syncwarp();  // the cluster's barrier wants whole warps: lanes come from ways of their own
         cluster_barrier();
     }
     __device__ __forceinline__ void load(int64_t g, float (&f)[8]) const {

@@ -389,7 +389,10 @@ struct Row {
 
     __device__ __forceinline__ void sync() const {
         __syncthreads();
-        if constexpr (C > 1) cluster_barrier();
+        if constexpr (C > 1) {
+            __syncwarp();  // the cluster's barrier wants whole warps: lanes come from ways of their own
+            cluster_barrier();
+        }
     }
     __device__ __forceinline__ Raw<T> load(int g) const {
         const int64_t v = int64_t(g) * kGroup + lane * 8;
