@@ -28,6 +28,8 @@ struct SharedX {
     Hist own, all;  // all: the leader's
     Settings set;
     WeightStep tab[32];
+    float m;  // the row's largest
+    double floor_d;
     // the leader's
     u64 run_sum[kRuns];
     uint32_t run_ties[kRuns];
@@ -80,16 +82,14 @@ struct RowX {
     int64_t n, V, G, per;
     int rank, tid, warp, lane;
     bool vec;
-    float m;  // the largest
     // At temperatures above 2^60 logits are taken as 2^-64 of themselves, and c as 2^64 of itself: the
     // distance of two logits that weighs something may not fit FP32, nor c
     float part;
     Weights W;
     u64 least;
     // u of 1 or more takes the last token left, also where its weight is no whole unit: tokens
-    // then count 1 each, and min_p is compared with x - max in FP64
+    // then count 1 each, and min_p is compared with x - max in FP64 (sh.floor_d)
     bool by_count;
-    double floor_d;
 
     __device__ __forceinline__ void sync() const {
         __syncthreads();
@@ -234,7 +234,7 @@ struct RowX {
         return w >= least ? w : 0;
     }
     __device__ __forceinline__ bool counts(float x) const {
-        return x == m || (m < INFINITY && static_cast<double>(x) - m >= floor_d);
+        return x == sh.m || (sh.m < INFINITY && static_cast<double>(x) - sh.m >= sh.floor_d);
     }
     // Sums over the tokens left, a run of groups each, to the leader.
     __device__ __forceinline__ void sum_left(uint32_t last, uint32_t to_sum, uint32_t to_ties) const {
@@ -276,7 +276,8 @@ struct RowX {
             }
             return;
         }
-        m = value_of(top);
+        const float m = value_of(top);
+        if (tid == 0) sh.m = m;
         W.c_hi = set.c;
         W.c_lo = set.c_lo;
         part = 1.f;
@@ -335,10 +336,11 @@ struct RowX {
         u64 w_tie = w_last >= least ? w_last : 0;
         if (last || least) sum_left(last, to_sum, to_ties);
         if (set.u >= 1) {
+            if (tid == 0)
+                sh.floor_d = set.min_p > 0 && set.T < INFINITY ? set.T * log(fmin(set.min_p, 1.0)) : -INFINITY;
             if (rank == 0) find_run(n_last, w_tie);  // their mass
             sync();
             by_count = true;
-            floor_d = set.min_p > 0 && set.T < INFINITY ? set.T * log(fmin(set.min_p, 1.0)) : -INFINITY;
             w_tie = last && counts(value_of(last)) ? 1 : 0;
             sum_left(last, to_sum, to_ties);
         }
@@ -458,7 +460,7 @@ struct RowX {
                 at += s;
                 if (at > target) {
                     const float x = f[j];
-                    const double z = x == m ? 0.0 : (static_cast<double>(x) - m) / set.T;
+                    const double z = x == sh.m ? 0.0 : (static_cast<double>(x) - sh.m) / set.T;
                     const double one = static_cast<double>(1ull << W.S);
                     a.tokens[n] = g * kGroupX + lane * 8 + j;
                     a.logp[n] = static_cast<float>(z - log(static_cast<double>(every) / one));
@@ -493,7 +495,7 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kThreadsX, 2)
             if (tid == 0) sh.set = settings_of(a, n);
             const T* row = static_cast<const T*>(a.logits) + n * a.ld;
             RowX<T> r{a, sh, row, n, a.V, (a.V + kGroupX - 1) / kGroupX, per, rank, tid, tid >> 5, tid & 31,
-                      reinterpret_cast<uintptr_t>(row) % 16 == 0, 0.f, 1.f, {}, 0, false, 0.0};
+                      reinterpret_cast<uintptr_t>(row) % 16 == 0, 1.f, {}, 0, false};
             r.run();
         }
     }
