@@ -29,7 +29,7 @@ struct SharedX {
     Settings set;
     WeightStep tab[32];
     float m;  // the row's largest
-    double floor_d;
+    uint32_t floor_key;
     // the leader's
     u64 run_sum[kRuns];
     uint32_t run_ties[kRuns];
@@ -88,8 +88,9 @@ struct RowX {
     Weights W;
     u64 least;
     // u of 1 or more takes the last token left, also where its weight is no whole unit: tokens
-    // then count 1 each, and min_p is compared with x - max in FP64 (sh.floor_d)
+    // then count 1 each, min_p leaving those from floor_key on
     bool by_count;
+    uint32_t floor_key;
 
     __device__ __forceinline__ void sync() const {
         __syncthreads();
@@ -229,22 +230,45 @@ struct RowX {
         const uint32_t key = key_of(x);
         ties += key == last;
         if (key <= last) return 0;
-        if (by_count) return counts(x) ? 1 : 0;
+        if (by_count) return key >= floor_key ? 1 : 0;
         const u64 w = weight(x);
         return w >= least ? w : 0;
     }
-    __device__ __forceinline__ bool counts(float x) const {
-        return x == sh.m || (sh.m < INFINITY && static_cast<double>(x) - sh.m >= sh.floor_d);
+    // The key of the lowest logit that min_p leaves: x - max compared in FP64.
+    __device__ uint32_t lowest_left(float m) const {
+        const Settings& set = sh.set;
+        uint32_t b = key_of(m);
+        if (!(m < INFINITY)) return b;
+        if (!(set.min_p > 0 && set.T < INFINITY)) return 1u;
+        const double floor_d = set.T * log(fmin(set.min_p, 1.0));
+        for (uint32_t a = 0; b - a > 1;) {
+            const uint32_t mid = a + (b - a) / 2;
+            if (static_cast<double>(value_of(mid)) - m >= floor_d)
+                b = mid;
+            else
+                a = mid;
+        }
+        return b;
     }
-    // Sums over the tokens left, a run of groups each, to the leader.
+    // Sums over the tokens left, or how many, a run of groups each, to the leader.
+    template <bool COUNT>
     __device__ __forceinline__ void sum_left(uint32_t last, uint32_t to_sum, uint32_t to_ties) const {
-        uint32_t ties = 0;
+        uint32_t ties = 0, some = 0;
         u64 sum = 0;
+        const uint32_t lowest = max(last + 1, floor_key);
         stream([&](const float (&f)[8]) {
 #pragma unroll 4
-            for (int j = 0; j < 8; ++j) sum += above_last(f[j], last, ties);
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (COUNT) {
+                    const uint32_t key = key_of(f[j]);
+                    some += key >= lowest;
+                    ties += key == last;
+                } else {
+                    sum += above_last(f[j], last, ties);
+                }
+            }
         });
-        sum = warp_sum64(sum);
+        sum = warp_sum64(COUNT ? some : sum);
         ties = __reduce_add_sync(0xffffffffu, last ? ties : 0u);
         if (lane == 0) {
             asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_sum), "l"(sum) : "memory");
@@ -334,15 +358,15 @@ struct RowX {
             least = static_cast<u64>(ceil(fmin(set.min_p, 1.0) * static_cast<double>(1ull << W.S)));
         const u64 w_last = last ? weight(value_of(last)) : 0;
         u64 w_tie = w_last >= least ? w_last : 0;
-        if (last || least) sum_left(last, to_sum, to_ties);
+        if (last || least) sum_left<false>(last, to_sum, to_ties);
         if (set.u >= 1) {
-            if (tid == 0)
-                sh.floor_d = set.min_p > 0 && set.T < INFINITY ? set.T * log(fmin(set.min_p, 1.0)) : -INFINITY;
+            if (tid == 0) sh.floor_key = lowest_left(sh.m);
             if (rank == 0) find_run(n_last, w_tie);  // their mass
             sync();
             by_count = true;
-            w_tie = last && counts(value_of(last)) ? 1 : 0;
-            sum_left(last, to_sum, to_ties);
+            floor_key = sh.floor_key;
+            w_tie = last && last >= floor_key ? 1 : 0;
+            sum_left<true>(last, to_sum, to_ties);
         }
         if (rank == 0) draw(every, last, n_last, w_tie);
         sync();
@@ -495,7 +519,7 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kThreadsX, 2)
             if (tid == 0) sh.set = settings_of(a, n);
             const T* row = static_cast<const T*>(a.logits) + n * a.ld;
             RowX<T> r{a, sh, row, n, a.V, (a.V + kGroupX - 1) / kGroupX, per, rank, tid, tid >> 5, tid & 31,
-                      reinterpret_cast<uintptr_t>(row) % 16 == 0, 1.f, {}, 0, false};
+                      reinterpret_cast<uintptr_t>(row) % 16 == 0, 1.f, {}, 0, false, 0};
             r.run();
         }
     }
