@@ -13,12 +13,13 @@
 // (cta_group::2): each holds 128 rows of either operand, and the accumulator's rows of its
 // own tokens, as rows of the output.  With the scales there is room for one accumulator
 // in TMEM: eight warps empty it into registers before the next tile's MMAs begin.
-// Bound by what L2 gives the SMs (about 12 TB/s of operands) and by the time the accumulator
-// is emptied: 4096 x 2048 x 32768 132 us, 2048 x 4096 x 151936 558 (4.6 PFLOP/s).
+// 4096 x 2048 x 32768 (mx) 124 us, 2048 x 4096 x 151936 (nv) 532: 4.4 and 4.8 PFLOP/s.  Of the
+// first's time the tensor pipe is active 45%; L2 moves 1.42 GB (11 TB/s), 0.27 of them the output, and
+// no MMA runs while the accumulator is emptied.
 // Few tokens (few_kernel): the 128 rows of a tile are vocabulary entries, the columns
 // tokens, so that no tensor work is spent on padding tokens and a warp's store of one
 // column is 32 neighbouring logits of a token.  The weights are read once: bound by memory
-// (48 x 4096 x 151936: 72 us, 4.9 TB/s).
+// (48 x 4096 x 151936: 71 us, 4.9 TB/s).
 #include <string.h>
 
 #include <mutex>
@@ -867,7 +868,7 @@ cudaError_t launch_fp4_linear(const Fp4Matrix& h, const Fp4Matrix& w, const void
     P.status = dev.status;
     P.wait_ns = wait_limit_ns();
     // us by few_kernel and pair_kernel, 32768 x 2048 and 151936 x 4096 weights: 16 tokens 12.0 and
-    // 14.7, 68.5 and 74.0; 64 13.8 and 14.7, 71.8 and 75.5; 128 17.5 and 15.6, 76.7 and 76.9
+    // 14.7, 68.5 and 74.0; 64 13.8 and 14.7, 71.8 and 75.5; 128 17.5 and 14.7, 76.7 and 74.1
     const bool few = h.rows <= 96;
 #define LL_RUN(F, T) (few ? run_few<F, T>(h, w, P, dev, s) : run_pair<F, T>(h, w, P, dev, s))
 #define LL_RUN_T(T) (h.format == LL_FP4_MX ? LL_RUN(LL_FP4_MX, T) : LL_RUN(LL_FP4_NV, T))

@@ -4,9 +4,12 @@
 // block is a maximum over 4 lanes (LL_FP4_MX, 32 columns) or 2 (LL_FP4_NV, 16), its codes
 // are one 32-bit store a lane, and the scales of four blocks one 32-bit store.
 //
-// Bound, for large matrices, by instructions: 151936 x 4096 BF16 in LL_FP4_NV 560-630 us (the
-// largest magnitude ahead of it 205 us, 6.1 TB/s), where the bytes would take 235; back 320-460
-// us, depending on what of it L2 holds.  Small ones are a launch (48 x 4096: 2.3 us).
+// 151936 x 4096 BF16 in LL_FP4_NV 559 us (the largest magnitude ahead of it 205 us, 6.1 TB/s), in
+// LL_FP4_MX 563, where the bytes would take 235; back 325-331.  The variant of 16 rows a warp, which
+// these sizes take, keeps part of its four rows in local memory (208-240 bytes a thread, at 48
+// registers for 5 blocks an SM): 40960 x 2048 under a profiler 90 us at 60% of issue slots, 0.73 GB
+// of local loads and stores beside 0.25 GB of DRAM's.  The one of 1 row does not (32768 x 2048: 75
+// us, 73%).  Back, 48 us for 40960 x 2048 at 65%.  Small ones are a launch (48 x 4096: 2.3 us).
 #include "fp4_device.cuh"
 
 namespace ll {

@@ -5,7 +5,8 @@
 // A cluster of 8 CTAs a row, each warp with one run of its groups of 256 logits.  The last
 // token left is found by its key, 11 bits a pass: histograms of the tokens and of their mass
 // in shared memory, added up in the leader's.  Bound by instructions: a weight takes about 45, so
-// that a pass over a row of 151936 is 27 us of one SM's issue, and 8 share it.
+// that a pass over a row of 151936 is 27 us of one SM's issue, and 8 share it.  48 rows of 151936 to
+// the top 1000 290 us, 512 3040; 48 at u = 1 92.
 #include "sample_device.cuh"
 #include "step_device.cuh"
 

@@ -21,10 +21,12 @@
 // One block a row, or for few rows a cluster of 8, whose first CTA (the leader) decides; the
 // ranges, and so all sums, are the same.
 //
-// Bound by the pass's instructions, about 9 a logit, and for few rows by the chain of steps after
-// it.  Rows of 151936, us: 1024 uncut (bf16) 159, of which HBM would take 46; 512 with top_p 0.9 310
-// (the histogram's additions in shared memory, a second pass); 48 (FP32) with top_k 50 and top_p
-// 0.95 31.
+// Rows of 151936, us: 1024 uncut (bf16) 160, of which HBM would take 46; 512 with top_p 0.9 311; 512
+// with min_p 0.001 198; 48 (FP32) with top_k 50 and top_p 0.95 31.  The launches one by one under a
+// profiler, whose caches are cold, us: uncut 95 (14 warp instructions for 32 logits, the schedulers
+// issue in 64% of cycles) and then 61 for the 29 rows of 1024 that the FP32 bound leaves to
+// clusters, each a whole pass again and a chain of short steps (25%); top_p 230 and 159 for 68 of
+// 512 rows; 8 to 9 for an exact kernel that finds no row.
 //
 // Errors: with weights off by e_w at most (relative) and a target t = u Z, the difference of
 // t and a sum P next to it is off by u e_w (Z - P) + (1 - u) e_w P: what P and Z share

@@ -605,8 +605,9 @@ int ll_fp4_dequantize(const void* codes, const void* scales, const float* scale,
  * Logits from 4-bit operands of one format:
  *   out[n, v] = sum_k h[n, k] W[v, k] (+ bias[v])
  * h [N, K] and W [V, K] as above.  The products of codes and block scales are exact and
- * summed in FP32 by the tensor cores; the sum is multiplied by the two `scale`s
- * (LL_FP4_NV), the bias is added, and the result rounded once to out_dtype.
+ * summed in FP32 by the tensor cores (a partial sum beyond FP32's range makes the result
+ * infinite); the sum is multiplied by the two `scale`s (LL_FP4_NV), whose own product may
+ * lie outside that range, the bias is added, and the result rounded once to out_dtype.
  *   bias [V] of bias_dtype, device, or NULL.
  *   out  [N, ldo] of out_dtype, device (columns [0, V) written; ldo >= V; elements
  *        aligned to their size).  It may not overlap an input.
@@ -664,11 +665,12 @@ size_t ll_sample_workspace_size(int64_t N, int64_t V, int dtype);
  *            the last token left.
  *   tokens   [N] int64, logp [N], logq [N] float, device (written).  Neither they nor the
  *            workspace may overlap each other or an input (LL_ERR_INVALID_ARG).
- * The weights are formed to 2^-37 of their size and summed as 64-bit integers, in units of
- * 2^-46 of the largest (or V 2^-62, if that is more); in FP32 where the error, of which a
- * bound is kept, cannot change the outcome.  So the tokens are those of the definition
- * unless u or a setting lies that close to a border.  logp and logq are within 2e-6 of the
- * definition before their rounding.  A row depends on its own inputs alone, not on the
+ * The weights are formed to 2^-37 of their size and summed as 64-bit integers, each rounded
+ * to a unit of 2^-46 of the largest (or V 2^-62, if that is more), so that a sum of V of them
+ * is off by V / 2 units at most; in FP32 where the error, of which a bound is kept, cannot
+ * change the outcome.  So the tokens are those of the definition unless u or a setting lies
+ * within these errors of a border.  logp and logq are within 2e-6 of the definition before
+ * their rounding, for V up to 4 million.  A row depends on its own inputs alone, not on the
  * batch, and runs give the same bits.
  * A top_k above 256, a u of 1 or more, more than 2 million tokens, logits of which the
  * largest is below -2^19 (FP16: -2^15) or more than 2^20 T in size, and temperatures above
