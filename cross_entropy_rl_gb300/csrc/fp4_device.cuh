@@ -59,8 +59,8 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
 }
 
 // The product of two matrices' scales as g * two, `two` a power of 2: 1 where the product lies
-// within 2^-100 .. 2^100.  A sum of products, 0 or 2^-20 to 2^54 in size, times `two` and then g
-// leaves FP32's range only where it does so times both scales (and then by 2^-126 at least).
+// within 2^-100 .. 2^100.  A sum of products is 0 or 2^-20 to 2^54 in size: times `two` and then g
+// it is beyond FP32's range, or below it, only where the exact result is.
 struct ScaleProduct {
     float g, two;
 };
